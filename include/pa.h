@@ -342,6 +342,94 @@ size_t pa_decode_mq_workspace_size(pa_geom geom, int32_t num_seqs, int32_t n_q,
                                    int32_t num_ctas);
 
 /*
+ * pa_decode_mass -- pa_decode that also adds every cached token's attention
+ * weight to its running mass, what eviction by accumulated attention weight
+ * goes by. With s_j as in pa_decode, for j < ctx_b and kv head v:
+ *     mass_out[b][v][j] = mass[b][v][j] + sum over the g heads of softmax(s)_j
+ *
+ *   mass      fp32 [num_seqs][n_kv][max_blocks_per_seq * 16] (read): entry j
+ *             stands for the token at block_tables[b][j / 16], offset j % 16
+ *   mass_out  the same shape (written): mass itself, to add in place, or
+ *             another buffer, which leaves mass as it was. Entries j >= ctx_b
+ *             are not written. Both 16-byte aligned.
+ * Weights are formed and added in fp32, in an order that does not depend on
+ * how the work was split. A bad block's tokens have weight 0; a sequence with
+ * a bad context length keeps its masses. Two sequences that share blocks have
+ * masses of their own. Every other argument and error is pa_decode's, plus
+ * num_ctas (0: the default grid; > 0: the CTA count, as in pa_decode_ex). The
+ * workspace is pa_decode_mass_workspace_size bytes: pa_decode's part, zeroed as
+ * pa_decode_workspace_init says, and the scores, 4 bytes per query head and
+ * block-table slot. The pages have no counterpart.
+ */
+pa_status pa_decode_mass(const void *q, const void *k_cache, const void *v_cache,
+                         const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                         float scale, void *out, const float *mass, float *mass_out,
+                         void *workspace, size_t workspace_bytes, pa_geom geom,
+                         int32_t *dev_status, void *stream, int32_t num_ctas);
+
+/* Workspace bytes pa_decode_mass needs (0 if an argument is invalid). */
+size_t pa_decode_mass_workspace_size(pa_geom geom, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                     int32_t num_ctas);
+
+/*
+ * pa_evict_select -- the tokens of each (sequence, kv head) that stay.
+ *
+ * With n = context_lens[b], k = min(n, budget), r = min(recent, k), the kept
+ * tokens of kv head v are the last r (n - r .. n - 1) and, of the others, the
+ * k - r with the largest mass[b][v][j]; equal masses go to the lowest index, -0
+ * equals 0, and NaN counts as less than everything.
+ *
+ *   mass        fp32 [num_seqs][n_kv][max_tokens]
+ *   max_tokens  1 .. 2^31 - 1
+ *   budget      > 0 tokens to keep; recent: 0 .. budget
+ *   keep        int32 [num_seqs][n_kv][budget] (written): the kept tokens in
+ *               ascending order, then -1
+ *   keep_lens   int32 [num_seqs] (written): k
+ *   dev_status  optional; a context length < 0 or > max_tokens sets
+ *               PA_DEV_BAD_CONTEXT and keeps nothing of that sequence
+ * num_seqs == 0 does nothing. The result is the same however it is computed.
+ */
+pa_status pa_evict_select(const float *mass, int64_t max_tokens, const int32_t *context_lens,
+                          int32_t num_seqs, int32_t n_kv, int32_t budget, int32_t recent,
+                          int32_t *keep, int32_t *keep_lens, int32_t *dev_status, void *stream);
+
+/*
+ * pa_evict_compact -- move the kept rows of every sequence, in order, into
+ * fresh blocks of the same pool: row i < keep_lens[b] of the new table is row
+ * keep[b][v][i] of the old one, for every kv head v, in K, V, their scales
+ * and, when mass is not NULL, the masses. The kv heads keep different tokens,
+ * so afterwards row i is another token for each head, and the new context
+ * length is keep_lens[b].
+ *
+ *   block_tables  int32 [num_seqs][max_blocks_per_seq] (read)
+ *   keep          int32 [num_seqs][n_kv][budget], keep_lens int32 [num_seqs]:
+ *                 as pa_evict_select writes them (any token below
+ *                 max_blocks_per_seq * 16 may be named)
+ *   new_tables    int32 [num_seqs][new_blocks_per_seq] (read): blocks that no
+ *                 block table names, each once (pa_allocator_allocate_private
+ *                 hands such blocks out); not block_tables itself
+ *                 (PA_ERR_SHAPE). Sequences that share old blocks each get
+ *                 their own copy. Slots behind a sequence's last row are left
+ *                 as they were.
+ *   mass          fp32 [num_seqs][n_kv][max_blocks_per_seq * 16], mass_out fp32
+ *                 [num_seqs][n_kv][new_blocks_per_seq * 16] (written; another
+ *                 buffer): entries i >= keep_lens[b] become 0, so that tokens
+ *                 appended later start there. Both or neither.
+ *   dev_status    optional: a count outside [0, budget] or over the new table's
+ *                 capacity moves nothing of its sequence and a token outside
+ *                 the old table is not moved (PA_DEV_BAD_CONTEXT); a block
+ *                 outside the pool is neither read nor written
+ *                 (PA_DEV_BAD_BLOCK). The mass of what did not move is 0.
+ */
+pa_status pa_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *keep, int32_t budget, const int32_t *keep_lens,
+                           const int32_t *new_tables, int32_t new_blocks_per_seq,
+                           int32_t num_seqs, const float *mass, float *mass_out, pa_geom geom,
+                           int32_t *dev_status, void *stream);
+
+/*
  * pa_sink_write -- store bf16 attention-sink rows of new tokens.
  *
  * For each row t with 0 <= positions[t] < n_sink and 0 <= seq_rows[t] <

@@ -75,6 +75,19 @@ pa_status pa_allocator_allocate_prompt(pa_allocator *a, const int32_t *token_ids
                                        int32_t *n_blocks, int32_t *cached_tokens);
 
 /*
+ * Block table for n_tokens >= 0 rows that no prompt can share: fresh blocks
+ * without a hash, each held once (for pa_evict_compact, whose rows are a choice
+ * among a sequence's tokens that differs by head, so no prefix may hit them).
+ *   block_table   host int32 [capacity], receives ceil(n_tokens / block_size)
+ *                 block ids
+ *   n_blocks      receives that count
+ * The blocks count as filled with n_tokens rows (token ids 0), so
+ * pa_allocator_append_slots goes on behind them.
+ */
+pa_status pa_allocator_allocate_private(pa_allocator *a, int32_t n_tokens, int32_t *block_table,
+                                        int32_t capacity, int32_t *n_blocks);
+
+/*
  * Append one decoded token to each of num_seqs sequences, in order.
  *   block_tables  host int32 [num_seqs][capacity], row i holds n_blocks[i]
  *                 valid entries; rows are updated in place (a new block is

@@ -12,6 +12,7 @@ the library has not been built, or no CUDA device is present, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -47,8 +48,11 @@ EXPORTED = ["pa_cache_write", "pa_decode_workspace_size", "pa_decode_workspace_i
             "pa_decode_mq", "pa_decode_mq_ex", "pa_decode_mq_workspace_size", "pa_decode_opt_workspace_size",
             "pa_status_string", "pa_status_from_device", "pa_version", "pa_wait_selftest",
             "pa_kv_read_probe", "pa_share_groups",
+            "pa_decode_mass", "pa_decode_mass_workspace_size", "pa_evict_select",
+            "pa_evict_compact",
             # host block manager (include/pa_alloc.h)
             "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate_prompt",
+            "pa_allocator_allocate_private",
             "pa_allocator_append_slots", "pa_allocator_fork", "pa_allocator_free",
             "pa_allocator_num_free", "pa_allocator_block_info", "pa_allocator_free_order",
             "pa_block_hash"]
@@ -130,6 +134,15 @@ def _lib():
         lib.pa_decode_opt_workspace_size.argtypes = [pa_geom, i32, P]
         lib.pa_decode_opt.restype = ctypes.c_int
         lib.pa_decode_opt.argtypes = dec[:14] + [P] + dec[14:]
+        lib.pa_decode_mass_workspace_size.restype = sz
+        lib.pa_decode_mass_workspace_size.argtypes = [pa_geom, i32, i32, i32]
+        lib.pa_decode_mass.restype = ctypes.c_int
+        lib.pa_decode_mass.argtypes = dec[:11] + [P, P] + dec[11:] + [i32]
+        lib.pa_evict_select.restype = ctypes.c_int
+        lib.pa_evict_select.argtypes = [P, i64, P, i32, i32, i32, i32, P, P, P, P]
+        lib.pa_evict_compact.restype = ctypes.c_int
+        lib.pa_evict_compact.argtypes = [P, P, P, P, P, i32, P, i32, P, P, i32, i32, P, P,
+                                         pa_geom, P, P]
         lib.pa_sink_write.restype = ctypes.c_int
         lib.pa_sink_write.argtypes = [P, P, P, P, i64, P, P, i32, i32, pa_geom, P]
         lib.pa_kv_read_probe.restype = ctypes.c_int
@@ -145,6 +158,8 @@ def _lib():
         lib.pa_allocator_destroy.argtypes = [P]
         lib.pa_allocator_allocate_prompt.restype = ctypes.c_int
         lib.pa_allocator_allocate_prompt.argtypes = [P, P, i32, P, i32, P, P]
+        lib.pa_allocator_allocate_private.restype = ctypes.c_int
+        lib.pa_allocator_allocate_private.argtypes = [P, i32, P, i32, P]
         lib.pa_allocator_append_slots.restype = ctypes.c_int
         lib.pa_allocator_append_slots.argtypes = [P, P, i32, P, P, i32, P, P, P, P]
         lib.pa_allocator_fork.restype = ctypes.c_int
@@ -197,11 +212,12 @@ class Prepared:
     The stream is the one given at preparation, else the current stream at
     each call. Returns what the unprepared call returns (the output tensor)."""
 
-    __slots__ = ("_fn", "_args", "_si", "_what", "_result", "_stream")
+    __slots__ = ("_fn", "_args", "_si", "_what", "_result", "_stream", "_keep")
 
-    def __init__(self, fn, args, stream_index, what, result, stream):
+    def __init__(self, fn, args, stream_index, what, result, stream, keep=None):
         self._fn, self._args, self._si = fn, list(args), stream_index
         self._what, self._result, self._stream = what, result, stream
+        self._keep = keep  # what lives as long as the call (its workspace)
 
     def __call__(self):
         self._args[self._si] = _stream_ptr(self._stream)
@@ -452,6 +468,225 @@ def pa_decode_mq(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return call if prepare else call()
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream):
+    """Context with t's device current and, where a stream is given, that stream:
+    what a call allocates then belongs to the stream that uses it."""
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("stream and tensors are on different devices")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return _NO_SWITCH
+
+
+def _same_device(t: torch.Tensor, **others) -> None:
+    for name, o in others.items():
+        if o is not None and o.device != t.device:
+            raise ValueError(f"{name} is on {o.device}, not on {t.device}")
+
+
+_STREAM_WS: dict = {}
+
+
+def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) -> torch.Tensor:
+    """Workspace of one kind of call on the current stream, whose first `counters`
+    bytes are zero (the calls leave them zero). Kept per stream, so calls on two streams do
+    not share one. A prepared call (own) gets a buffer to itself, and a stream
+    that is being captured one of the graph's own, so those share none either."""
+    if own or torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:counters].zero_()
+        return ws
+    key = (kind, device.index, torch.cuda.current_stream().cuda_stream)
+    with _WS_LOCK:
+        ent = _STREAM_WS.get(key)
+        if ent is None or ent[0].numel() < nbytes:
+            ent = _STREAM_WS[key] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
+        if ent[1] < counters:
+            ent[0][:counters].zero_()
+        ent[1] = counters  # the rest is scratch
+        return ent[0]
+
+
+def _check_quant(g: pa_geom, k_scale, v_scale, shape) -> None:
+    for nm, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if g.kv_dtype == PA_KV_BF16:
+            if s is not None:
+                raise ValueError(f"{nm}: a bf16 pool has no scales")
+            continue
+        if s is None:
+            raise ValueError(f"{nm} is required for an int8/int4 pool")
+        _need_cuda(nm, s, torch.float32)
+        if s.shape != shape[:3]:
+            raise ValueError(f"{nm} must be [num_blocks, n_kv, block_size]")
+
+
+def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                   mass: torch.Tensor, mass_out: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   dev_status: Optional[torch.Tensor] = None, stream=None, num_ctas: int = 0,
+                   prepare: bool = False):
+    """pa_decode that also adds each cached token's attention weight, summed over
+    the query heads of its kv head, to its mass.
+
+    mass: float32 [B, n_kv, max_blocks * 16], entry j for the token at
+    block_tables[b][j // 16], offset j % 16; the sums go to mass_out (default: in
+    place). Entries at and behind a context's end are not written. Everything
+    else, and the result, as pa_decode."""
+    _need_cuda("q", q, torch.bfloat16)
+    _need_cuda("k_cache", k_cache)
+    _need_cuda("v_cache", v_cache, k_cache.dtype)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    _need_cuda("mass", mass, torch.float32)
+    if mass_out is None:
+        mass_out = mass
+    else:
+        _need_cuda("mass_out", mass_out, torch.float32)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [num_seqs, n_h, d_h], block_tables [num_seqs, max_blocks]")
+    B, n_h, d = q.shape
+    g = geometry(k_cache, n_h)
+    mb = block_tables.shape[1]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have the shape of k_cache")
+    if d != g.d_h or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("q, block_tables, context_lens disagree on num_seqs or d_h")
+    if mass.shape != (B, g.n_kv, mb * 16) or mass_out.shape != mass.shape:
+        raise ValueError("mass, mass_out must be [num_seqs, n_kv, max_blocks * 16]")
+    _check_quant(g, k_scale, v_scale, k_cache.shape)
+    if out is not None:
+        _need_cuda("out", out, torch.bfloat16)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    if workspace is not None:
+        _need_cuda("workspace", workspace)
+    if dev_status is not None:
+        _need_cuda("dev_status", dev_status, torch.int32)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, mass=mass, mass_out=mass_out, out=out, k_scale=k_scale,
+                 v_scale=v_scale, workspace=workspace, dev_status=dev_status)
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            key = ("mass", q.device.index, g.num_blocks, n_h, g.n_kv, d, g.kv_dtype, B, mb, num_ctas)
+            nbytes = _WS_SIZES.get(key)
+            if nbytes is None:
+                nbytes = _lib().pa_decode_mass_workspace_size(g, B, mb, int(num_ctas))
+                if nbytes == 0 and B > 0:
+                    raise PAError(-4, "pa_decode_mass_workspace_size")
+                _WS_SIZES[key] = nbytes
+            workspace = _stream_workspace("mass", nbytes, _counter_bytes(g, B), q.device,
+                                          prepare)
+        call = Prepared(_lib().pa_decode_mass,
+                        [_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                         _ptr(block_tables), mb, _ptr(context_lens), B, float(scale), _ptr(out),
+                         _ptr(mass), _ptr(mass_out), _ptr(workspace),
+                         workspace.numel() * workspace.element_size(), g, _ptr(dev_status), None,
+                         int(num_ctas)],
+                        17, "pa_decode_mass", out, stream, workspace)
+        return call if prepare else call()
+
+
+def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int, recent: int = 0,
+                    keep: Optional[torch.Tensor] = None,
+                    keep_lens: Optional[torch.Tensor] = None,
+                    dev_status: Optional[torch.Tensor] = None, stream=None,
+                    prepare: bool = False):
+    """The tokens of each (sequence, kv head) that stay when a sequence is cut to
+    `budget` tokens: the last `recent` and the heaviest of the others (mass
+    float32 [B, n_kv, max_tokens]; ties to the lowest index).
+    -> (keep int32 [B, n_kv, budget], ascending, then -1; keep_lens int32 [B])."""
+    _need_cuda("mass", mass, torch.float32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    if mass.dim() != 3 or context_lens.shape != mass.shape[:1]:
+        raise ValueError("mass must be [num_seqs, n_kv, max_tokens], context_lens [num_seqs]")
+    B, n_kv, tokens = mass.shape
+    budget, recent = int(budget), int(recent)
+    if budget <= 0 or not 0 <= recent <= budget:
+        raise ValueError("budget must be > 0 and recent within 0 .. budget")
+    for nm, t, shape in (("keep", keep, (B, n_kv, budget)), ("keep_lens", keep_lens, (B,))):
+        if t is not None:
+            _need_cuda(nm, t, torch.int32)
+            if t.shape != shape:
+                raise ValueError(f"{nm} must be {list(shape)}")
+    if dev_status is not None:
+        _need_cuda("dev_status", dev_status, torch.int32)
+    _same_device(mass, context_lens=context_lens, keep=keep, keep_lens=keep_lens,
+                 dev_status=dev_status)
+    with _on(mass, stream):
+        if keep is None:
+            keep = torch.empty((B, n_kv, budget), dtype=torch.int32, device=mass.device)
+        if keep_lens is None:
+            keep_lens = torch.empty(B, dtype=torch.int32, device=mass.device)
+        call = Prepared(_lib().pa_evict_select,
+                        [_ptr(mass), tokens, _ptr(context_lens), B, n_kv, budget, recent,
+                         _ptr(keep), _ptr(keep_lens), _ptr(dev_status), None],
+                        10, "pa_evict_select", (keep, keep_lens), stream)
+        return call if prepare else call()
+
+
+def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     keep: torch.Tensor, keep_lens: torch.Tensor, new_tables: torch.Tensor,
+                     mass: Optional[torch.Tensor] = None, mass_out: Optional[torch.Tensor] = None,
+                     k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None,
+                     prepare: bool = False):
+    """Move the kept rows (keep, keep_lens as pa_evict_select gives them) from
+    block_tables [B, max_blocks] to new_tables [B, new_blocks], blocks of the same
+    pool that no table names (BlockAllocator.allocate_private). With mass [B, n_kv,
+    max_blocks * 16], the kept tokens' masses go to mass_out [B, n_kv,
+    new_blocks * 16], 0 behind them."""
+    _need_cuda("k_cache", k_cache)
+    _need_cuda("v_cache", v_cache, k_cache.dtype)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("keep", keep, torch.int32)
+    _need_cuda("keep_lens", keep_lens, torch.int32)
+    _need_cuda("new_tables", new_tables, torch.int32)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have the shape of k_cache")
+    g = geometry(k_cache, n_h=k_cache.shape[1])
+    _check_quant(g, k_scale, v_scale, k_cache.shape)
+    if block_tables.dim() != 2 or new_tables.dim() != 2 or keep.dim() != 3:
+        raise ValueError("block_tables, new_tables must be [num_seqs, blocks], keep "
+                         "[num_seqs, n_kv, budget]")
+    B, budget = keep.shape[0], keep.shape[2]
+    mb, nb = block_tables.shape[1], new_tables.shape[1]
+    if keep.shape[1] != g.n_kv or block_tables.shape[0] != B or new_tables.shape[0] != B or \
+            keep_lens.shape != (B,):
+        raise ValueError("keep, keep_lens and the tables disagree on num_seqs or n_kv")
+    if (mass is None) != (mass_out is None):
+        raise ValueError("mass and mass_out go together")
+    if mass is not None:
+        _need_cuda("mass", mass, torch.float32)
+        _need_cuda("mass_out", mass_out, torch.float32)
+        if mass.shape != (B, g.n_kv, mb * 16) or mass_out.shape != (B, g.n_kv, nb * 16):
+            raise ValueError("mass must be [num_seqs, n_kv, max_blocks * 16], mass_out "
+                             "[num_seqs, n_kv, new_blocks * 16]")
+    if dev_status is not None:
+        _need_cuda("dev_status", dev_status, torch.int32)
+    _same_device(k_cache, v_cache=v_cache, block_tables=block_tables, keep=keep,
+                 keep_lens=keep_lens, new_tables=new_tables, mass=mass, mass_out=mass_out,
+                 k_scale=k_scale, v_scale=v_scale, dev_status=dev_status)
+    with _on(k_cache, stream):
+        call = Prepared(_lib().pa_evict_compact,
+                        [_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                         _ptr(block_tables), mb, _ptr(keep), budget, _ptr(keep_lens),
+                         _ptr(new_tables), nb, B, _ptr(mass), _ptr(mass_out), g,
+                         _ptr(dev_status), None],
+                        16, "pa_evict_compact", None, stream)
+        return call if prepare else call()
+
+
 def pa_sink_write(k: torch.Tensor, v: torch.Tensor, seq_rows: torch.Tensor,
                   positions: torch.Tensor, sink_k: torch.Tensor, sink_v: torch.Tensor,
                   stream=None) -> None:
@@ -640,6 +875,18 @@ class BlockAllocator:
                                                    ctypes.byref(cached)),
                "pa_allocator_allocate_prompt")
         return table[:n.value].copy(), cached.value
+
+    def allocate_private(self, n_tokens: int) -> np.ndarray:
+        """Block table (int32 array) of fresh blocks for n_tokens rows that no prompt
+        can share: the new home of a sequence that pa_evict_compact cuts."""
+        n_tokens = int(n_tokens)
+        cap = max(0, n_tokens + self.block_size - 1) // self.block_size
+        table = np.empty(max(cap, 1), np.int32)
+        n = ctypes.c_int32()
+        _check(_lib().pa_allocator_allocate_private(self._h, n_tokens, _np_ptr(table), cap,
+                                                    ctypes.byref(n)),
+               "pa_allocator_allocate_private")
+        return table[:n.value].copy()
 
     def append_slots(self, tables: np.ndarray, n_blocks: np.ndarray, token_ids):
         """Append one token to each row of `tables` (int32 [B, capacity], updated in

@@ -36,6 +36,11 @@ SOURCES = [
     "pa_decode_int8_mq_d64.cu",
     "pa_decode_int4_mq_d128.cu",
     "pa_decode_int4_mq_d64.cu",
+    "pa_decode_mass_bf16.cu",
+    "pa_decode_mass_int8.cu",
+    "pa_decode_mass_int4.cu",
+    "pa_mass.cu",
+    "pa_evict.cu",
     "pa_share.cu",
     "pa_selftest.cu",
     "pa_decode_noalloc.cu",

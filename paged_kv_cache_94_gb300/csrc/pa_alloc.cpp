@@ -335,6 +335,30 @@ pa_status pa_allocator_allocate_prompt(pa_allocator *a, const int32_t *token_ids
     return PA_OK;
 }
 
+pa_status pa_allocator_allocate_private(pa_allocator *a, int32_t n_tokens, int32_t *block_table,
+                                        int32_t capacity, int32_t *n_blocks)
+{
+    if (!a || !n_blocks || (n_tokens > 0 && !block_table))
+        return PA_ERR_NULL;
+    if (n_tokens < 0 || capacity < 0)
+        return PA_ERR_SHAPE;
+    const int32_t bs = a->bs;
+    const int32_t n = (int32_t)(((int64_t)n_tokens + bs - 1) / bs);
+    if (n > capacity)
+        return PA_ERR_SHAPE;
+    if ((int64_t)n > a->pool_size)
+        return PA_ERR_OUT_OF_BLOCKS;
+    for (int32_t k = 0; k < n; ++k) {
+        const int32_t b = a->take();
+        const int32_t len = k + 1 < n ? bs : n_tokens - k * bs;
+        std::memset(a->tokens.data() + (size_t)b * bs, 0, sizeof(int32_t) * (size_t)len);
+        a->blk[b].ntok = len;
+        block_table[k] = b;
+    }
+    *n_blocks = n;
+    return PA_OK;
+}
+
 pa_status pa_allocator_append_slots(pa_allocator *a, int32_t *block_tables, int32_t capacity,
                                     int32_t *n_blocks, const int32_t *token_ids,
                                     int32_t num_seqs, int64_t *slots, int32_t *cow_pairs,

@@ -97,7 +97,7 @@ struct OccEntry {
     size_t smem;
     int per_sm;
 };
-constexpr int kOccCache = 64;
+constexpr int kOccCache = 256;
 OccEntry g_occ[kOccCache];
 int g_occ_n = 0;
 struct AttrEntry {
@@ -140,9 +140,9 @@ pa_status ctas_per_sm(const DecodeKernel *kd, size_t smem, int &n)
     return PA_OK;
 }
 
-pa_status default_ctas(const pa_geom &g, int num_seqs, int &grid, int nq = 1)
+// One wave of resident CTAs of a kernel for a batch size.
+pa_status resident_ctas(const DecodeKernel *kd, int num_seqs, int &grid)
 {
-    const DecodeKernel *kd = kernel_for(g, nq);
     if (!kd)
         return PA_ERR_UNSUPPORTED;
     int dev, sms, per;
@@ -154,6 +154,11 @@ pa_status default_ctas(const pa_geom &g, int num_seqs, int &grid, int nq = 1)
         return st;
     grid = sms * per;
     return PA_OK;
+}
+
+pa_status default_ctas(const pa_geom &g, int num_seqs, int &grid, int nq = 1)
+{
+    return resident_ctas(kernel_for(g, nq), num_seqs, grid);
 }
 
 size_t counters_bytes(int64_t units) { return (size_t)((units * 4 + 255) / 256 * 256); }
@@ -175,6 +180,26 @@ struct ShareLayout {
 };
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Decode that keeps its scores: pa_decode's counters and records, then (M, 1/L)
+// per query head and the scores [num_seqs][n_kv][max_blocks * 16][g].
+struct MassLayout {
+    size_t ml, scores, end;
+};
+
+MassLayout mass_layout(const pa_geom &g, int num_seqs, int max_blocks, int grid)
+{
+    MassLayout L;
+    L.ml = round256(workspace_bytes_for(g, num_seqs, grid));
+    L.scores = L.ml + round256((size_t)num_seqs * g.n_h * sizeof(float2));
+    L.end = L.scores + (size_t)num_seqs * g.n_h * max_blocks * 16 * sizeof(float);
+    return L;
+}
+
+struct MassArgs {
+    const float *mass;
+    float *mass_out;
+};
 
 // Shared memory and resident CTAs per SM of the shared-prefix kernel for a
 // batch (its 2 * num_seqs units' prefix arrays grow with the batch);
@@ -298,7 +323,7 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
                       const int32_t *context_lens, int32_t num_seqs, float scale, void *out,
                       void *workspace, size_t workspace_bytes, pa_geom g, int32_t *dev_status,
                       void *stream, int32_t num_ctas, const pa_decode_opts *opts = nullptr,
-                      int nq = 1)
+                      int nq = 1, const MassArgs *ma = nullptr)
 {
     pa_status st = check_geom(g);
     if (st != PA_OK)
@@ -336,7 +361,13 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
         !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
         return PA_ERR_ALIGNMENT;
 
-    const DecodeKernel *kd = kernel_for(g, nq);
+    if (ma && (!ma->mass || !ma->mass_out))
+        return PA_ERR_NULL;
+    if (ma && (!aligned(ma->mass, 16) || !aligned(ma->mass_out, 16)))
+        return PA_ERR_ALIGNMENT;
+
+    const DecodeKernel *kd =
+        ma ? pa::find_mass_kernel(g.kv_dtype, g.d_h, group_of(g)) : kernel_for(g, nq);
     if (!kd)
         return PA_ERR_UNSUPPORTED;
     int dev, sms, per;
@@ -359,7 +390,8 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
     if (share) // default: one wave of resident CTAs
         grid = num_ctas > 0 ? num_ctas : sms * per_sh;
     const ShareLayout SL = share ? share_layout(g, num_seqs, grid) : ShareLayout{};
-    if (workspace_bytes < (share ? SL.end : workspace_bytes_for(g, num_seqs, grid, nq)))
+    const MassLayout ML = ma ? mass_layout(g, num_seqs, max_blocks, grid) : MassLayout{};
+    if (workspace_bytes < (ma ? ML.end : share ? SL.end : workspace_bytes_for(g, num_seqs, grid, nq)))
         return PA_ERR_WORKSPACE;
 
     CUtensorMap tk, tv;
@@ -397,6 +429,9 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
     p.pre = nullptr;
     p.groups = nullptr;
     p.members = nullptr;
+    uint8_t *wsb = static_cast<uint8_t *>(workspace);
+    p.ml = ma ? reinterpret_cast<float2 *>(wsb + ML.ml) : nullptr;
+    p.scores = ma ? reinterpret_cast<float *>(wsb + ML.scores) : nullptr;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     p.num_real = num_seqs;
     p.grid_fixed = num_ctas > 0 ? 1 : 0;
@@ -427,7 +462,10 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
         p.num_ctas = grid;
         return kp->launch(tk, tv, p, grid, smem_sh, cs) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
-    const cudaError_t e = kd->launch(tk, tv, p, grid, smem, cs);
+    cudaError_t e = kd->launch(tk, tv, p, grid, smem, cs);
+    if (e == cudaSuccess && ma)
+        e = pa::launch_mass(p.scores, p.ml, context_lens, ma->mass, ma->mass_out, num_seqs, g.n_kv,
+                            p.g, max_blocks, sms, cs);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -682,6 +720,108 @@ pa_status pa_decode_mq_ex(const void *q, const void *k_cache, const void *v_cach
     return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
                        context_lens, num_seqs, scale, out, workspace, workspace_bytes, geom,
                        dev_status, stream, num_ctas, nullptr, n_q);
+}
+
+size_t pa_decode_mass_workspace_size(pa_geom geom, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                     int32_t num_ctas)
+{
+    if (check_geom(geom) != PA_OK || num_seqs < 0 || num_seqs > kMaxSeqs || num_ctas < 0 ||
+        max_blocks_per_seq <= 0 || (int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31))
+        return 0;
+    const DecodeKernel *kd = pa::find_mass_kernel(geom.kv_dtype, geom.d_h, group_of(geom));
+    int grid = num_ctas;
+    if (!kd || (grid == 0 && resident_ctas(kd, num_seqs, grid) != PA_OK))
+        return 0;
+    return mass_layout(geom, num_seqs, max_blocks_per_seq, grid).end;
+}
+
+pa_status pa_decode_mass(const void *q, const void *k_cache, const void *v_cache,
+                         const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                         float scale, void *out, const float *mass, float *mass_out,
+                         void *workspace, size_t workspace_bytes, pa_geom geom,
+                         int32_t *dev_status, void *stream, int32_t num_ctas)
+{
+    const NvtxRange range("pa_decode_mass");
+    const MassArgs ma = {mass, mass_out};
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
+                       context_lens, num_seqs, scale, out, workspace, workspace_bytes, geom,
+                       dev_status, stream, num_ctas, nullptr, 1, &ma);
+}
+
+pa_status pa_evict_select(const float *mass, int64_t max_tokens, const int32_t *context_lens,
+                          int32_t num_seqs, int32_t n_kv, int32_t budget, int32_t recent,
+                          int32_t *keep, int32_t *keep_lens, int32_t *dev_status, void *stream)
+{
+    const NvtxRange range("pa_evict_select");
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || n_kv <= 0 || max_tokens <= 0 ||
+        max_tokens > INT32_MAX || budget <= 0 || recent < 0 || recent > budget)
+        return PA_ERR_SHAPE;
+    if ((int64_t)num_seqs * n_kv > (int64_t(1) << 27))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!mass || !context_lens || !keep || !keep_lens)
+        return PA_ERR_NULL;
+    if (!aligned(mass, 4) || !aligned(context_lens, 4) || !aligned(keep, 4) ||
+        !aligned(keep_lens, 4))
+        return PA_ERR_ALIGNMENT;
+    int dev, sms;
+    const pa_status st = current_device(dev, sms);
+    if (st != PA_OK)
+        return st;
+    return pa::launch_evict_select(mass, max_tokens, context_lens, num_seqs, n_kv, budget, recent,
+                                   keep, keep_lens, sms, dev_status,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+pa_status pa_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *keep, int32_t budget, const int32_t *keep_lens,
+                           const int32_t *new_tables, int32_t new_blocks_per_seq,
+                           int32_t num_seqs, const float *mass, float *mass_out, pa_geom geom,
+                           int32_t *dev_status, void *stream)
+{
+    const NvtxRange range("pa_evict_compact");
+    const pa_status st = check_geom(geom);
+    if (st != PA_OK)
+        return st;
+    if (num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq <= 0 || budget <= 0 ||
+        new_blocks_per_seq <= 0)
+        return PA_ERR_SHAPE;
+    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31) ||
+        (int64_t)num_seqs * new_blocks_per_seq >= (int64_t(1) << 31))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!k_cache || !v_cache || !block_tables || !keep || !keep_lens || !new_tables ||
+        (mass == nullptr) != (mass_out == nullptr))
+        return PA_ERR_NULL;
+    const bool i8 = geom.kv_dtype != PA_KV_BF16; // INT8 or INT4: fp32 scales
+    if (i8 && (!k_scale || !v_scale))
+        return PA_ERR_NULL;
+    if (!i8 && (k_scale || v_scale))
+        return PA_ERR_SHAPE;
+    // moved in place, a row could be overwritten before it is read
+    if (new_tables == block_tables || (mass && mass == mass_out))
+        return PA_ERR_SHAPE;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
+        !aligned(keep, 4) || !aligned(keep_lens, 4) || !aligned(new_tables, 4) ||
+        (i8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) ||
+        (mass && (!aligned(mass, 4) || !aligned(mass_out, 4))))
+        return PA_ERR_ALIGNMENT;
+    const int row_bytes = geom.kv_dtype == PA_KV_BF16   ? 2 * geom.d_h
+                          : geom.kv_dtype == PA_KV_INT8 ? geom.d_h
+                                                        : geom.d_h / 2;
+    return pa::launch_evict_compact(k_cache, v_cache, k_scale, v_scale, block_tables,
+                                    max_blocks_per_seq, keep, budget, keep_lens, new_tables,
+                                    new_blocks_per_seq, mass, mass_out, num_seqs, geom.num_blocks,
+                                    geom.n_kv, row_bytes, dev_status,
+                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 pa_status pa_sink_write(const void *k, const void *v, const int32_t *seq_rows,

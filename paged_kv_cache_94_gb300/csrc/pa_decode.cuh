@@ -88,6 +88,11 @@ struct DecodeParams {
     const int32_t *members;
     int32_t num_real;
     int32_t grid_fixed;          // 1: the caller chose num_ctas (no whole-unit grid)
+    // Attention weights (MASS kernels, see pa_mass.cu): every attended token's
+    // scores (log2 domain) go to scores[b][kv head][token][g], and each query
+    // row's softmax base and 1 / sum to ml[b][head].
+    float *scores;
+    float2 *ml;
 };
 
 // Pass 0: decode of each sequence; pass 2: shared-prefix groups, then each
@@ -445,6 +450,21 @@ __device__ __forceinline__ int atomic_add_acq_rel_gpu(int32_t *addr, int v)
     return old;
 }
 
+// Scores of one token's GQ query heads that this lane holds (two heads of the
+// tile's columns), to row `tok` of the unit's scores.
+template <int GQ>
+__device__ __forceinline__ void store_scores(float *srow, int tok, int nt, int t4, float s0,
+                                             float s1)
+{
+    const int h = nt * 8 + 2 * t4;
+    if constexpr (GQ == 1) {
+        if (h == 0)
+            srow[tok] = s0;
+    } else if (h < GQ) {
+        *reinterpret_cast<float2 *>(srow + tok * GQ + h) = make_float2(s0, s1);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // End of a segment: merge the NW warp states (`merge`, [NW][GQ][D+2]: m, l,
 // acc[D], each warp against its own running base) and write the output, or
@@ -585,7 +605,15 @@ struct MergeRun {
     static_assert(GQ * D / RUN <= NT && D % RUN == 0, "one run per thread");
 };
 
-template <int D, int GQ, int NW, int NQ>
+// Softmax base and reciprocal sum of query row h (MASS kernels).
+template <int GQ, int NQ>
+__device__ __forceinline__ void emit_ml(const DecodeParams &p, int b, int kvh, int h, float M,
+                                        float L)
+{
+    p.ml[qo_row<GQ, NQ>(p, b, kvh, h)] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
+}
+
+template <int D, int GQ, int NW, int NQ, bool MASS = false>
 __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int32_t *P,
                                                const float *merge, int32_t *misc, float *sink_sc,
                                                int b, int kvh, int nb, int64_t Wv, int64_t G,
@@ -645,6 +673,9 @@ __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int3
             }
         }
         if (whole) {
+            if constexpr (MASS)
+                if (d0 == 0)
+                    emit_ml<GQ, NQ>(p, b, kvh, h, M, L);
 #pragma unroll
             for (int e = 0; e < RUN; e += 2)
                 emit2<D, GQ, NQ>(p, b, kvh, h, d0 + e, L, O[e], O[e + 1]);
@@ -680,6 +711,9 @@ __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int3
     st.clear();
     fold_rows<RUN, MergeRun<D, GQ, NT>::RB>(
         st, p.partials + ((size_t)c_first + u) * (GQ * REC) + h * REC, (size_t)GQ * REC, nseg, d0);
+    if constexpr (MASS)
+        if (d0 == 0)
+            emit_ml<GQ, NQ>(p, b, kvh, h, st.M, st.L);
 #pragma unroll
     for (int e = 0; e < RUN; e += 2)
         emit2<D, GQ, NQ>(p, b, kvh, h, d0 + e, st.L, st.O[e], st.O[e + 1]);

@@ -139,9 +139,12 @@ struct Bf16Policy {
 
     // One 16-token block: K tile at kt, V tile at kt + TILE (shared addresses).
     // Rows [lo, valid) of the block are attended; the others are masked. rem =
-    // ctx - the block's first position (the multi-query causal limit).
+    // ctx - the block's first position (the multi-query causal limit). MASS:
+    // the attended tokens' scores also go to srow[token][GQ].
+    template <bool MASS = false>
     __device__ static void compute(State &st, uint32_t kt, uint32_t /*extra*/, int lo, int valid,
-                                   int rem, float scale_log2, uint32_t /*mask: 1*/)
+                                   int rem, float scale_log2, uint32_t /*mask: 1*/,
+                                   float *srow = nullptr)
     {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
         const int mi = lane >> 3, rr = lane & 7;
@@ -190,6 +193,12 @@ struct Bf16Policy {
             }
             if constexpr (NQ > 1)
                 causal_mask<GQ, NQ>(sc, nt, gid, t4, rem);
+            if constexpr (MASS) {
+                if (lo_ok)
+                    store_scores<GQ>(srow, gid, nt, t4, sc[0], sc[1]);
+                if (hi_ok)
+                    store_scores<GQ>(srow, gid + 8, nt, t4, sc[2], sc[3]);
+            }
             // Lazy rescale: the running base m only moves when a tile's max
             // exceeds it by more than 2^kRescaleLog2; otherwise weights up to
             // 2^kRescaleLog2 are accumulated against the old base (exact: acc
@@ -325,8 +334,9 @@ namespace pa {
 // ---------------------------------------------------------------------------
 // PASS 0: decode of each sequence. PASS 2: shared-prefix decode, the groups'
 // shared blocks (all query rows of the group at once) and then every
-// sequence's remaining blocks, in one launch.
-template <class Pol, int PASS = 0>
+// sequence's remaining blocks, in one launch. MASS (pass 0 only): the scores
+// and softmax bases also go to p.scores and p.ml.
+template <class Pol, int PASS = 0, bool MASS = false>
 __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecodeParams p)
@@ -542,10 +552,23 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
                 const int rem = (int)min(ctx - t0, TOK + kBlockTokens); // >= TOK + NQ - 1
                 const int valid = (int)min(rem, TOK);
                 // (mask: the item's blocks that were loaded; a bad one is not attended)
-                if (lo < valid)
+                if constexpr (MASS) {
+                    float *srow = p.scores + (((size_t)b * p.n_kv + kvh) * p.max_blocks *
+                                                  kBlockTokens + t0) * GQ;
+                    Pol::template compute<true>(st, ring_base + (uint32_t)(cstage * Pol::STAGE),
+                                                extra_base + (uint32_t)(cstage * Pol::EXTRA), lo,
+                                                valid, rem, p.scale_log2, (uint32_t)mask, srow);
+                } else if (lo < valid)
                     Pol::compute(st, ring_base + (uint32_t)(cstage * Pol::STAGE),
                                  extra_base + (uint32_t)(cstage * Pol::EXTRA), lo, valid, rem,
                                  p.scale_log2, (uint32_t)mask);
+            } else if constexpr (MASS) {
+                // an item of bad blocks: its tokens have no weight
+                const int32_t t0 = BPI * (int32_t)(x - unit_start) * kBlockTokens;
+                float *srow = p.scores + (((size_t)b * p.n_kv + kvh) * p.max_blocks *
+                                              kBlockTokens + t0) * GQ;
+                for (int i = lane; i < min(ctx - t0, TOK) * GQ; i += 32)
+                    srow[i] = -INFINITY;
             }
             __syncwarp();
             if (!dead && r.issued < r.n_items)
@@ -572,7 +595,7 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
         if constexpr (PASS == 2)
             finish_fused<D, GQ, NW>(p, P, merge, misc, b_cur, kvh_cur, Wv, G, whole);
         else
-            finish_segment<D, GQ, NW, Pol::NQ>(p, P, merge, misc, sink_sc, b_cur, kvh_cur,
+            finish_segment<D, GQ, NW, Pol::NQ, MASS>(p, P, merge, misc, sink_sc, b_cur, kvh_cur,
                                                (int)nb_cur, Wv, G, whole, ws,
                                                s_hi > ws ? s_hi : ws);
         seg_lo = seg_hi;
@@ -593,7 +616,7 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
 // append, or the group detection) finishes, and wait for that kernel's
 // completion in their first instruction. After anything else on the stream
 // it behaves as a plain launch.
-template <class Pol, int PASS>
+template <class Pol, int PASS, bool MASS = false>
 cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p,
                           int grid, size_t smem, cudaStream_t stream)
 {
@@ -607,7 +630,7 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const De
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<Pol, PASS>, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<Pol, PASS, MASS>, tk, tv, p);
 }
 
 } // namespace pa

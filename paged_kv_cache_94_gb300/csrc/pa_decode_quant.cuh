@@ -388,8 +388,11 @@ struct QuantMmaPolicy {
     // extra + 64*(BPI+j) (V). Tokens [lo, valid) of the item are attended,
     // those of block j only if bit j of mask is set (the block was loaded);
     // rem = ctx - (the item's first position), for the causal mask (NQ > 1).
+    // MASS: the scores of tokens [lo, valid) also go to srow[token][GQ].
+    template <bool MASS = false>
     __device__ static void compute(State &st, uint32_t kt, uint32_t extra, int lo, int valid,
-                                   int rem, float scale_log2, uint32_t mask)
+                                   int rem, float scale_log2, uint32_t mask,
+                                   float *srow = nullptr)
     {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
 
@@ -482,6 +485,12 @@ struct QuantMmaPolicy {
                 }
                 if constexpr (NQ > 1) // block j starts 16j tokens into the item
                     causal_mask<GQ, NQ>(pr[j][nt], nt, gid, t4, rem - 16 * j);
+                if constexpr (MASS) { // (a block that was not loaded: -inf)
+                    if (tl < valid)
+                        store_scores<GQ>(srow, tl, nt, t4, pr[j][nt][0], pr[j][nt][1]);
+                    if (th < valid)
+                        store_scores<GQ>(srow, th, nt, t4, pr[j][nt][2], pr[j][nt][3]);
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     need |= fmaxf(pr[j][nt][e], pr[j][nt][e + 2]) > st.m[nt][e] + kRescaleLog2;

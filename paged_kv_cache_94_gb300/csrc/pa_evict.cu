@@ -1,0 +1,372 @@
+// Eviction from a paged cache by accumulated attention weight.
+//
+// select_kernel: which tokens of each (sequence, kv head) stay. With n = ctx_b,
+//   k = min(n, budget), r = min(recent, k): tokens n - r .. n - 1, and of the
+//   m = n - r before them the k - r of largest mass, ties to the lowest index,
+//   in ascending order. The k - r th largest key (masses as unsigned integers
+//   in their order) is found digit by digit, 11 + 11 + 10 bits, from counts in
+//   shared memory; one more sweep counts what lies above it and writes the
+//   indices at their ranks. Ranks come from warp ballots and prefix sums, so
+//   the result does not depend on any order of execution.
+//   A row is 4 n bytes, read once: latency-bound. So a long row is cut over a
+//   cluster of up to 8 CTAs (counts joined in the first one's shared memory) and
+//   each thread keeps its keys in registers between the sweeps; rows too long
+//   for that read them again from L2.
+//
+// compact_kernel: row i of the new block table = row keep[i] of the old one,
+//   for K, V, their scales and the masses. Bound by HBM: each kept row is read
+//   and written once. A CTA moves 1024 16-byte pieces of K and as many of V:
+//   64 bf16 rows of 128, more of narrower ones. The rows' places are looked up
+//   once into shared memory; then every thread has eight 16-byte loads in
+//   flight before its first store.
+#include <cooperative_groups.h>
+
+#include "pa_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+namespace {
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeys = 32; // keys a thread keeps in registers
+
+// Masses as unsigned integers of the same order. -0 equals +0; NaN lies below
+// everything, so a token whose mass is not a number goes first.
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.f); // -0 + 0 = +0
+    if (x != x)
+        return 0u;
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+struct SelShared {
+    int32_t hist[kBins];
+    int32_t total[kBins]; // the cluster's counts (first CTA)
+    int32_t warp_sum[kSelWarps];
+    int32_t digit, need;  // result of a digit's scan
+    int32_t gt[kSelWarps], eq[kSelWarps];
+    int32_t cta_gt, cta_eq;
+};
+
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelThreads)
+select_kernel(const float *__restrict__ mass, int64_t stride,
+              const int32_t *__restrict__ context_lens, int n_kv, int budget, int recent,
+              int32_t *__restrict__ keep, int32_t *__restrict__ keep_lens, int32_t *dev_status)
+{
+    __shared__ SelShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t u = blockIdx.x / C; // b * n_kv + kv head
+    const int b = (int)(u / n_kv);
+    int32_t n = __ldg(context_lens + b);
+    if (n < 0 || n > stride) {
+        if (tid == 0 && dev_status)
+            atomicOr(dev_status, PA_DEV_BAD_CONTEXT_BIT);
+        n = 0;
+    }
+    const int32_t k = min(n, budget), r = min(recent, k);
+    const int32_t m = n - r, want = k - r; // choose `want` of tokens [0, m)
+    int32_t *out = keep + u * budget;
+
+    // what needs no choice: the recent tokens, the unused tail, the count
+    for (int32_t i = want + rank * kSelThreads + tid; i < budget; i += C * kSelThreads)
+        out[i] = i < k ? m + (i - want) : -1;
+    if (tid == 0 && rank == 0 && u % n_kv == 0)
+        keep_lens[b] = k;
+    if (want == m) { // nothing to evict (the same in every CTA of the cluster)
+        for (int32_t i = rank * kSelThreads + tid; i < want; i += C * kSelThreads)
+            out[i] = i;
+        return;
+    }
+    if (want == 0)
+        return;
+
+    // this warp's run of tokens: whole rounds of 32
+    const int32_t warps = C * kSelWarps;
+    const int32_t rounds = (int32_t)(((int64_t)m + 32 * warps - 1) / (32 * warps));
+    const int64_t first = (int64_t)(rank * kSelWarps + warp) * rounds * 32 + lane;
+    const float *row = mass + u * stride;
+    auto load = [&](int it) -> uint32_t { // (only called for tokens below m)
+        return key_of(__ldg(row + first + (int64_t)it * 32));
+    };
+    uint32_t keys[CACHED ? kKeys : 1];
+    if constexpr (CACHED) {
+#pragma unroll
+        for (int it = 0; it < kKeys; ++it)
+            keys[it] = it < rounds && first + it * 32 < m ? load(it) : 0u;
+    }
+    // f(round, key, valid) over this thread's tokens, all lanes of a warp together
+    auto sweep = [&](auto f) {
+        if constexpr (CACHED) {
+#pragma unroll
+            for (int it = 0; it < kKeys; ++it)
+                if (it < rounds)
+                    f(it, keys[it], first + it * 32 < m);
+        } else {
+            for (int it = 0; it < rounds; ++it) {
+                const bool in = first + (int64_t)it * 32 < m;
+                f(it, in ? load(it) : 0u, in);
+            }
+        }
+    };
+
+    uint32_t prefix = 0;
+    int32_t need = want;
+    int top = 32; // bits [top, 32) of the threshold are known
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int bits = pass < 2 ? 11 : 10, low = top - bits;
+        for (int i = tid; i < kBins; i += kSelThreads)
+            sh.hist[i] = sh.total[i] = 0;
+        cluster.sync(); // the first CTA's totals are zero before anyone adds to them
+        sweep([&](int, uint32_t key, bool in) {
+            if (in && (top == 32 || (key >> top) == (prefix >> top)))
+                atomicAdd(&sh.hist[(key >> low) & ((1u << bits) - 1)], 1);
+        });
+        __syncthreads();
+        int32_t *total = C == 1 ? sh.hist : cluster.map_shared_rank(sh.total, 0);
+        if (C > 1) {
+            for (int i = tid; i < kBins; i += kSelThreads)
+                if (sh.hist[i])
+                    atomicAdd(total + i, sh.hist[i]);
+            cluster.sync();
+        }
+        if (rank == 0) { // the digit: counts from the top until `need` are covered
+            const int32_t *t = C == 1 ? sh.hist : sh.total;
+            constexpr int PER = kBins / kSelThreads;
+            int32_t c[PER], sum = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                c[j] = t[kBins - 1 - (tid * PER + j)];
+                sum += c[j];
+            }
+            int32_t x = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (lane == 31)
+                sh.warp_sum[warp] = x;
+            __syncthreads();
+            int32_t before = x - sum;
+            for (int w = 0; w < warp; ++w)
+                before += sh.warp_sum[w];
+            if (before < need && need <= before + sum) { // exactly one thread
+                int j = 0;
+                while (before + c[j] < need)
+                    before += c[j++];
+                const int32_t digit = kBins - 1 - (tid * PER + j), left = need - before;
+                for (int q = 0; q < C; ++q) {
+                    SelShared *s = cluster.map_shared_rank(&sh, q);
+                    s->digit = digit;
+                    s->need = left;
+                }
+            }
+        }
+        cluster.sync();
+        prefix |= (uint32_t)sh.digit << low;
+        need = sh.need;
+        top = low;
+    }
+
+    // ranks: tokens above the threshold, and the first `need` of those equal to it
+    int32_t gt = 0, eq = 0;
+    sweep([&](int, uint32_t key, bool in) {
+        gt += in && key > prefix;
+        eq += in && key == prefix;
+    });
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+        sh.gt[warp] = gt;
+        sh.eq[warp] = eq;
+    }
+    __syncthreads();
+    int32_t gt0 = 0, eq0 = 0; // before this warp
+    for (int w = 0; w < kSelWarps; ++w) {
+        gt0 += w < warp ? sh.gt[w] : 0;
+        eq0 += w < warp ? sh.eq[w] : 0;
+    }
+    if (C > 1) {
+        if (tid == 0) {
+            int32_t g = 0, e = 0;
+            for (int w = 0; w < kSelWarps; ++w) {
+                g += sh.gt[w];
+                e += sh.eq[w];
+            }
+            sh.cta_gt = g;
+            sh.cta_eq = e;
+        }
+        cluster.sync();
+        for (int q = 0; q < rank; ++q) {
+            gt0 += *cluster.map_shared_rank(&sh.cta_gt, q);
+            eq0 += *cluster.map_shared_rank(&sh.cta_eq, q);
+        }
+    }
+    const uint32_t below = (1u << lane) - 1;
+    sweep([&](int it, uint32_t key, bool in) {
+        const uint32_t g = __ballot_sync(0xffffffffu, in && key > prefix);
+        const uint32_t e = __ballot_sync(0xffffffffu, in && key == prefix);
+        const int32_t gb = gt0 + __popc(g & below), eb = eq0 + __popc(e & below);
+        if (in && (key > prefix || (key == prefix && eb < need)))
+            out[gb + min(eb, need)] = (int32_t)(first + (int64_t)it * 32);
+        gt0 += __popc(g);
+        eq0 += __popc(e);
+    });
+    if (C > 1)
+        cluster.sync(); // no CTA leaves while another reads its shared memory
+}
+
+// ---------------------------------------------------------------------------
+constexpr int kCompThreads = 256;
+constexpr int kPieces = 1024;                             // 16-byte pieces of K (and of V) per CTA
+constexpr int kPerThread = 2 * kPieces / kCompThreads;    // 8
+
+// PPR: 16-byte pieces per row
+template <int PPR>
+__global__ void __launch_bounds__(kCompThreads)
+compact_kernel(uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+               const int32_t *__restrict__ tables, int max_blocks,
+               const int32_t *__restrict__ keep, int budget, const int32_t *__restrict__ keep_lens,
+               const int32_t *__restrict__ new_tables, int new_blocks,
+               const float *__restrict__ mass, float *mass_out, int64_t num_blocks, int n_kv,
+               int tiles, int32_t *dev_status)
+{
+    constexpr int ROWS = kPieces / PPR;
+    __shared__ int32_t src[ROWS], dst[ROWS]; // pool rows; -1: not moved
+    const int64_t u = blockIdx.x / tiles;    // b * n_kv + kv head
+    const int b = (int)(u / n_kv), h = (int)(u - (int64_t)b * n_kv);
+    const int32_t row0 = (int32_t)(blockIdx.x - u * tiles) * ROWS;
+    const int64_t old_cap = (int64_t)max_blocks * 16, new_cap = (int64_t)new_blocks * 16;
+    int32_t kept = __ldg(keep_lens + b);
+    if (kept < 0 || kept > budget || kept > new_cap) {
+        if (threadIdx.x == 0 && dev_status)
+            atomicOr(dev_status, PA_DEV_BAD_CONTEXT_BIT);
+        kept = 0;
+    }
+    for (int t = threadIdx.x; t < ROWS; t += kCompThreads) {
+        const int32_t i = row0 + t;
+        int32_t s = -1, d = -1;
+        float w = 0.f;
+        if (i < kept) {
+            const int32_t j = __ldg(keep + u * budget + i);
+            if (j < 0 || j >= old_cap) {
+                if (dev_status)
+                    atomicOr(dev_status, PA_DEV_BAD_CONTEXT_BIT);
+            } else {
+                const int32_t sb = __ldg(tables + (int64_t)b * max_blocks + j / 16);
+                const int32_t db = __ldg(new_tables + (int64_t)b * new_blocks + i / 16);
+                if (sb < 0 || sb >= num_blocks || db < 0 || db >= num_blocks) {
+                    if (dev_status)
+                        atomicOr(dev_status, PA_DEV_BAD_BLOCK_BIT);
+                } else {
+                    s = (sb * n_kv + h) * 16 + j % 16;
+                    d = (db * n_kv + h) * 16 + i % 16;
+                    if (k_scale) {
+                        k_scale[d] = k_scale[s];
+                        v_scale[d] = v_scale[s];
+                    }
+                    if (mass)
+                        w = __ldg(mass + u * old_cap + j);
+                }
+            }
+        }
+        src[t] = s;
+        dst[t] = d;
+        if (mass_out && i < new_cap)
+            mass_out[u * new_cap + i] = w;
+    }
+    if (row0 >= kept)
+        return;
+    __syncthreads();
+    uint4 x[kPerThread];
+    // piece c of the CTA's 2 * kPieces: row c / (2 PPR), then K's pieces, then V's
+#pragma unroll
+    for (int e = 0; e < kPerThread; ++e) {
+        const int c = e * kCompThreads + threadIdx.x, t = c / (2 * PPR), o = c % (2 * PPR);
+        const uint8_t *pool = o < PPR ? k_cache : v_cache;
+        if (src[t] >= 0)
+            x[e] = __ldcs(reinterpret_cast<const uint4 *>(pool) + (int64_t)src[t] * PPR + o % PPR);
+    }
+#pragma unroll
+    for (int e = 0; e < kPerThread; ++e) {
+        const int c = e * kCompThreads + threadIdx.x, t = c / (2 * PPR), o = c % (2 * PPR);
+        uint8_t *pool = o < PPR ? k_cache : v_cache;
+        if (src[t] >= 0)
+            reinterpret_cast<uint4 *>(pool)[(int64_t)dst[t] * PPR + o % PPR] = x[e];
+    }
+}
+
+} // namespace
+
+cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t *context_lens,
+                                int num_seqs, int n_kv, int budget, int recent, int32_t *keep,
+                                int32_t *keep_lens, int sms, int32_t *dev_status,
+                                cudaStream_t stream)
+{
+    const int64_t rows = (int64_t)num_seqs * n_kv;
+    // CTAs per row: more while the rows leave SMs idle and each CTA still has
+    // eight keys per thread
+    int C = 1;
+    while (C < 8 && rows * C < 2 * sms && stride / C > 8 * kSelThreads)
+        C *= 2;
+    if (rows * C > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const bool cached = stride <= (int64_t)C * kSelThreads * kKeys;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cached ? select_kernel<true> : select_kernel<false>, mass,
+                              stride, context_lens, n_kv, budget, recent, keep, keep_lens,
+                              dev_status);
+}
+
+cudaError_t launch_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                 const int32_t *tables, int max_blocks, const int32_t *keep,
+                                 int budget, const int32_t *keep_lens, const int32_t *new_tables,
+                                 int new_blocks, const float *mass, float *mass_out, int num_seqs,
+                                 int64_t num_blocks, int n_kv, int row_bytes, int32_t *dev_status,
+                                 cudaStream_t stream)
+{
+    const int ppr = row_bytes / 16;
+    const int rows = kPieces / ppr;
+    // without masses only rows to move; with them the entries behind those are zeroed
+    const int64_t new_cap = (int64_t)new_blocks * 16;
+    const int64_t cover = mass_out || new_cap < budget ? new_cap : budget;
+    const int64_t tiles = (cover + rows - 1) / rows;
+    const int64_t grid = (int64_t)num_seqs * n_kv * tiles;
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)grid, kCompThreads, 0, stream>>>(
+            static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), k_scale, v_scale,
+            tables, max_blocks, keep, budget, keep_lens, new_tables, new_blocks, mass, mass_out,
+            num_blocks, n_kv, (int)tiles, dev_status);
+        return cudaGetLastError();
+    };
+    switch (ppr) {
+    case 16: return go(compact_kernel<16>);
+    case 8: return go(compact_kernel<8>);
+    case 4: return go(compact_kernel<4>);
+    case 2: return go(compact_kernel<2>);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+} // namespace pa

@@ -56,6 +56,25 @@ const DecodeKernel *find_decode_kernel_bf16_mq(int d_h, int group, int nq);
 const DecodeKernel *find_decode_kernel_int8_mq(int d_h, int group, int nq);
 const DecodeKernel *find_decode_kernel_int4_mq(int d_h, int group, int nq);
 
+// Decode kernels that keep their scores, and the pass that turns those into
+// attention weights (pa_mass.cu); NULL when not compiled.
+const DecodeKernel *find_mass_kernel(int kind, int d_h, int group);
+cudaError_t launch_mass(const float *scores, const float2 *ml, const int32_t *context_lens,
+                        const float *mass, float *mass_out, int num_seqs, int n_kv, int g,
+                        int max_blocks, int sms, cudaStream_t stream);
+
+// Eviction by accumulated attention weight (pa_evict.cu).
+cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t *context_lens,
+                                int num_seqs, int n_kv, int budget, int recent, int32_t *keep,
+                                int32_t *keep_lens, int sms, int32_t *dev_status,
+                                cudaStream_t stream);
+cudaError_t launch_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                 const int32_t *tables, int max_blocks, const int32_t *keep,
+                                 int budget, const int32_t *keep_lens, const int32_t *new_tables,
+                                 int new_blocks, const float *mass, float *mass_out, int num_seqs,
+                                 int64_t num_blocks, int n_kv, int row_bytes, int32_t *dev_status,
+                                 cudaStream_t stream);
+
 cudaError_t launch_cache_write(const void *k, const void *v, const int64_t *slots, int64_t T,
                                int n_kv, int d_h, int kind, int64_t num_slots, void *k_cache,
                                void *v_cache, float *k_scale, float *v_scale, int32_t *dev_status,
