@@ -342,6 +342,51 @@ size_t pa_decode_mq_workspace_size(pa_geom geom, int32_t num_seqs, int32_t n_q,
                                    int32_t num_ctas);
 
 /*
+ * pa_cross_attention -- any number of query tokens per sequence attend to all of a
+ * paged K/V cache of another length: the states of an encoder, or rows that an
+ * eviction kept (pa_evict_compact), whose order says nothing of the queries'.
+ *
+ * Tokens cu_q[b] <= t < cu_q[b + 1] belong to sequence b. For each of them and every
+ * query head h, with v = h / g:
+ *     s_j = scale * < q[t][h][:], K_b[j][v] >        for j < ctx_b, no mask
+ *     out[t][h][:] = sum_j softmax(s)_j * V_b[j][v][:]
+ *
+ *   q, out    bf16 [num_q][n_h][d_h] (16-byte aligned)
+ *   num_q     0 .. 2^31 / n_h - 1 query tokens in all
+ *   cu_q      int32 [num_seqs + 1] (device): offsets, not decreasing, within
+ *             0 .. num_q; a sequence may have none. Rows of out that no sequence
+ *             has (before cu_q[0], from cu_q[num_seqs] on) are left as they were.
+ *   the pools, their scales (4-byte aligned), block_tables, context_lens, scale
+ *             as in pa_decode, for bf16, INT8 and INT4 pools; ctx_b == 0 gives
+ *             zero rows
+ *   workspace >= pa_cross_workspace_size(geom, num_ctas) bytes, 256-byte
+ *             aligned, its first 4 * (CTAs) bytes zero on entry (they are left
+ *             zero). Calls that share one must be ordered on one stream.
+ *   dev_status optional: a context length outside its table (zero rows) or a
+ *             sequence whose offsets decrease or leave 0 .. num_q (it writes
+ *             nothing) sets PA_DEV_BAD_CONTEXT; a bad block contributes nothing
+ *             (PA_DEV_BAD_BLOCK). Rows that two sequences claim, as they can
+ *             behind a decreasing offset, get either one's result.
+ *   num_ctas  0: one CTA per SM; 1 .. 8192: that many
+ * Scores, softmax sums and outputs accumulate in fp32; a weight (times its V
+ * scale) is rounded once to bf16, 2^-8 relative, before the products with V.
+ * Results do not depend on how the work was split beyond fp32 rounding, and are
+ * the same from call to call. The pages have no counterpart: they attend a
+ * request's own tokens.
+ */
+pa_status pa_cross_attention(const void *q, int64_t num_q, const int32_t *cu_q,
+                             const void *k_cache, const void *v_cache, const float *k_scale,
+                             const float *v_scale, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *context_lens,
+                             int32_t num_seqs, float scale, void *out, void *workspace,
+                             size_t workspace_bytes, pa_geom geom, int32_t *dev_status,
+                             void *stream, int32_t num_ctas);
+
+/* Workspace bytes pa_cross_attention needs on the current device (it depends on
+ * the SM count when num_ctas is 0); 0 if an argument is invalid. */
+size_t pa_cross_workspace_size(pa_geom geom, int32_t num_ctas);
+
+/*
  * pa_decode_mass -- pa_decode that also adds every cached token's attention
  * weight to its running mass, what eviction by accumulated attention weight
  * goes by. With s_j as in pa_decode, for j < ctx_b and kv head v:

@@ -49,7 +49,7 @@ EXPORTED = ["pa_cache_write", "pa_decode_workspace_size", "pa_decode_workspace_i
             "pa_status_string", "pa_status_from_device", "pa_version", "pa_wait_selftest",
             "pa_kv_read_probe", "pa_share_groups",
             "pa_decode_mass", "pa_decode_mass_workspace_size", "pa_evict_select",
-            "pa_evict_compact",
+            "pa_evict_compact", "pa_cross_attention", "pa_cross_workspace_size",
             # host block manager (include/pa_alloc.h)
             "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate_prompt",
             "pa_allocator_allocate_private",
@@ -138,6 +138,11 @@ def _lib():
         lib.pa_decode_mass_workspace_size.argtypes = [pa_geom, i32, i32, i32]
         lib.pa_decode_mass.restype = ctypes.c_int
         lib.pa_decode_mass.argtypes = dec[:11] + [P, P] + dec[11:] + [i32]
+        lib.pa_cross_workspace_size.restype = sz
+        lib.pa_cross_workspace_size.argtypes = [pa_geom, i32]
+        lib.pa_cross_attention.restype = ctypes.c_int
+        lib.pa_cross_attention.argtypes = [P, i64, P, P, P, P, P, P, i32, P, i32, f32, P, P, sz,
+                                           pa_geom, P, P, i32]
         lib.pa_evict_select.restype = ctypes.c_int
         lib.pa_evict_select.argtypes = [P, i64, P, i32, i32, i32, i32, P, P, P, P]
         lib.pa_evict_compact.restype = ctypes.c_int
@@ -593,6 +598,71 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                          workspace.numel() * workspace.element_size(), g, _ptr(dev_status), None,
                          int(num_ctas)],
                         17, "pa_decode_mass", out, stream, workspace)
+        return call if prepare else call()
+
+
+def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, scale: float,
+                       out: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                       v_scale: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       dev_status: Optional[torch.Tensor] = None, stream=None, num_ctas: int = 0,
+                       prepare: bool = False):
+    """Cross attention: q [T, n_h, d_h] bf16, of which tokens cu_q[b] .. cu_q[b + 1] - 1
+    (cu_q int32 [B + 1], on the device) belong to sequence b, attend to all
+    context_lens[b] cached rows of that sequence (an encoder's states, or rows an
+    eviction kept; no causal mask) -> out of q's shape. Rows that no sequence has
+    are left as they were (in a new out: not initialised). The pool (bf16, INT8,
+    INT4), its scales and tables are pa_decode's."""
+    _need_cuda("q", q, torch.bfloat16)
+    _need_cuda("cu_q", cu_q, torch.int32)
+    _need_cuda("k_cache", k_cache)
+    _need_cuda("v_cache", v_cache, k_cache.dtype)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [num_q, n_h, d_h], block_tables [num_seqs, max_blocks]")
+    T, n_h, d = q.shape
+    B, mb = block_tables.shape
+    g = geometry(k_cache, n_h)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have the shape of k_cache")
+    if d != g.d_h or context_lens.shape != (B,) or cu_q.shape != (B + 1,):
+        raise ValueError("q, cu_q, block_tables, context_lens disagree on num_seqs or d_h")
+    _check_quant(g, k_scale, v_scale, k_cache.shape)
+    if out is not None:
+        _need_cuda("out", out, torch.bfloat16)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    if workspace is not None:
+        _need_cuda("workspace", workspace)
+    if dev_status is not None:
+        _need_cuda("dev_status", dev_status, torch.int32)
+    _same_device(q, cu_q=cu_q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, out=out, k_scale=k_scale, v_scale=v_scale,
+                 workspace=workspace, dev_status=dev_status)
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            key = ("cross", q.device.index, d, num_ctas)
+            nbytes = _WS_SIZES.get(key)
+            if nbytes is None:
+                nbytes = _lib().pa_cross_workspace_size(g, int(num_ctas))
+                if nbytes == 0:
+                    raise PAError(-4, "pa_cross_workspace_size")
+                _WS_SIZES[key] = nbytes
+            # (one counter per CTA in front of at least 2 * 256 * (d + 2) floats per CTA)
+            counters = (nbytes // (512 * (d + 2) * 4) * 4 + 255) // 256 * 256
+            workspace = _stream_workspace("cross", nbytes, counters, q.device, prepare)
+        call = Prepared(_lib().pa_cross_attention,
+                        [_ptr(q), T, _ptr(cu_q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                         _ptr(v_scale), _ptr(block_tables), mb, _ptr(context_lens), B,
+                         float(scale), _ptr(out), _ptr(workspace),
+                         workspace.numel() * workspace.element_size(), g, _ptr(dev_status), None,
+                         int(num_ctas)],
+                        17, "pa_cross_attention", out, stream, workspace)
         return call if prepare else call()
 
 

@@ -28,6 +28,7 @@ using pa::DecodeKernel;
 using pa::DecodeParams;
 
 constexpr int kMaxSeqs = 8192;
+constexpr int kMaxCrossCtas = 8192;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -316,6 +317,25 @@ pa_status encode_pool(CUtensorMap &m, const void *base, const pa_geom &g)
     if (g_maps_n < kMapCache)
         ++g_maps_n;
     return PA_OK;
+}
+
+// Query rows [num_q][n_h][d_h] of cross attention: a box is the g heads of one kv
+// head for 128 / g tokens, 64 columns wide, 128-byte swizzle.
+pa_status encode_queries(CUtensorMap &m, const void *q, const pa_geom &g, int64_t num_q)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return PA_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)g.d_h, (cuuint64_t)g.n_h, (cuuint64_t)num_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)g.d_h * 2, (cuuint64_t)g.n_h * g.d_h * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group_of(g), (cuuint32_t)(128 / group_of(g))};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
@@ -747,6 +767,85 @@ pa_status pa_decode_mass(const void *q, const void *k_cache, const void *v_cache
     return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
                        context_lens, num_seqs, scale, out, workspace, workspace_bytes, geom,
                        dev_status, stream, num_ctas, nullptr, 1, &ma);
+}
+
+size_t pa_cross_workspace_size(pa_geom geom, int32_t num_ctas)
+{
+    int dev, sms;
+    if (check_geom(geom) != PA_OK || num_ctas < 0 || num_ctas > kMaxCrossCtas)
+        return 0;
+    if (num_ctas == 0 && current_device(dev, sms) != PA_OK)
+        return 0;
+    return pa::cross_workspace_bytes(geom.d_h, num_ctas > 0 ? num_ctas : sms);
+}
+
+pa_status pa_cross_attention(const void *q, int64_t num_q, const int32_t *cu_q,
+                             const void *k_cache, const void *v_cache, const float *k_scale,
+                             const float *v_scale, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *context_lens,
+                             int32_t num_seqs, float scale, void *out, void *workspace,
+                             size_t workspace_bytes, pa_geom geom, int32_t *dev_status,
+                             void *stream, int32_t num_ctas)
+{
+    const NvtxRange range("pa_cross_attention");
+    pa_status st = check_geom(geom);
+    if (st != PA_OK)
+        return st;
+    if (num_q < 0 || num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq <= 0 ||
+        num_ctas < 0 || num_ctas > kMaxCrossCtas)
+        return PA_ERR_SHAPE;
+    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31) ||
+        num_q >= (int64_t(1) << 31) / geom.n_h)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_q == 0)
+        return PA_OK;
+    if (!q || !cu_q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||
+        !workspace)
+        return !workspace ? PA_ERR_WORKSPACE : PA_ERR_NULL;
+    const bool i8 = geom.kv_dtype != PA_KV_BF16; // INT8 or INT4: fp32 scales
+    if (i8 && (!k_scale || !v_scale))
+        return PA_ERR_NULL;
+    if (!i8 && (k_scale || v_scale))
+        return PA_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
+        return PA_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(dev, sms)) != PA_OK)
+        return st;
+    const int grid = num_ctas > 0 ? num_ctas : sms;
+    if (workspace_bytes < pa::cross_workspace_bytes(geom.d_h, grid))
+        return PA_ERR_WORKSPACE;
+    CUtensorMap tq, tk, tv;
+    if ((st = encode_queries(tq, q, geom, num_q)) != PA_OK ||
+        (st = encode_pool(tk, k_cache, geom)) != PA_OK ||
+        (st = encode_pool(tv, v_cache, geom)) != PA_OK)
+        return st;
+    pa::CrossArgs a;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cu_q = cu_q;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.out = out;
+    a.workspace = workspace;
+    a.dev_status = dev_status;
+    a.num_q = num_q;
+    a.num_blocks = geom.num_blocks;
+    a.num_seqs = num_seqs;
+    a.n_kv = geom.n_kv;
+    a.g = group_of(geom);
+    a.d_h = geom.d_h;
+    a.kind = geom.kv_dtype;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_ctas = grid;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    return pa::launch_cross(tq, tk, tv, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 pa_status pa_evict_select(const float *mass, int64_t max_tokens, const int32_t *context_lens,

@@ -1,0 +1,829 @@
+// Cross attention: any number of query tokens per sequence over a paged K/V cache
+// of another length (an encoder's states, or rows an eviction kept).
+//
+//     s_j = scale <q[t][h], K_b[j][h / g]>,  j < ctx_b (no mask)
+//     out[t][h] = sum_j softmax(s)_j V_b[j][h / g],  cu_q[b] <= t < cu_q[b + 1]
+//
+// What bounds it: 4 d_h FLOP per (query row, key) against 2 rows of K/V bytes per
+// (kv head, key). A tile of 256 query rows is past the ridge (the tensor cores
+// bound it), a few rows leave it at the K/V stream.
+//
+// Split. The query rows of a kv head (tokens x the g heads that share it) are
+// packed: row t * g + h. A unit is (sequence, kv head, up to 256 packed rows),
+// one or two halves of 128 rows = one tensor-core tile each; its items are
+// the 128-key tiles of the context. Items lie on one line, an item as long as
+// its halves, and CTA c of G takes [c W / G, (c + 1) W / G) of it, so any mix of
+// lengths is balanced and a few long contexts still use every SM. A unit cut
+// by CTA borders leaves (m, l, O) records; the last CTA to finish it merges them
+// (log-sum-exp). No CTA waits for another.
+//
+// One CTA per SM, 12 warps:
+//   warps 0-3, 4-7  softmax of half 0 and half 1, a thread per query row
+//   warp 8          issues the matrix instructions (one lane)
+//   warp 9          bf16 pools: TMA copies of Q and of the paged K/V blocks
+//                   (a block is 16 rows: 2 KiB boxes in the 128-byte swizzle)
+//   warps 9-11      INT8/INT4 pools: read the codes, write them as bf16 (exact:
+//                   8 significant bits) into the same tiles; the K scale
+//                   multiplies the scores, the V scale the weights
+// Tensor memory (512 columns): scores of both halves (128 fp32 columns each), their
+// outputs (d_h columns each). The weights P overwrite their half's
+// scores as bf16 and are the A operand of P V: one rounding of 2^-8 relative
+// per weight, of the size of the output's own; sums l take the unrounded
+// weights. While one half is in its softmax the other has the tensor cores.
+//
+// The softmax base of a row moves only when a tile's maximum exceeds it by more
+// than 2^8 (exact: P, l and O share one base), so O is rarely rescaled.
+#include "pa_decode.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;       // query rows of a half, keys of a tile
+constexpr int kTileBlocks = kRows / kBlockTokens;
+constexpr int kUnitRows = 2 * kRows;
+constexpr int kLoaders = 96;     // INT8/INT4 loader threads
+constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
+constexpr float kMoveLog2 = 8.f; // see above
+
+struct CrossParams {
+    const void *k_cache;
+    const void *v_cache;
+    const float *k_scale;
+    const float *v_scale;
+    const int32_t *cu_q;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    __nv_bfloat16 *out;
+    float *records;    // [num_ctas][2][256][D + 2]
+    int32_t *counters; // [num_ctas], zero between calls
+    int32_t *dev_status;
+    int64_t num_q;
+    int64_t num_blocks;
+    int32_t num_seqs;
+    int32_t n_kv;
+    int32_t g;
+    int32_t max_blocks;
+    int32_t num_ctas;
+    float scale_log2;
+};
+
+struct Seq {
+    int32_t ctx, q0, nq;
+    int32_t tiles;  // 128-key tiles
+    int32_t halves; // 128-row halves of one kv head's query rows
+    __device__ int64_t cost(int n_kv) const { return (int64_t)n_kv * tiles * halves; }
+};
+
+// Sequence b's sizes; bad ones (reported where `report`) count as nothing.
+__device__ __forceinline__ Seq load_seq(const CrossParams &p, int b, bool report)
+{
+    Seq s;
+    const int32_t ctx = __ldg(p.context_lens + b);
+    const int32_t q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
+    const bool q_ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_q;
+    const bool c_ok = ctx >= 0 && ctx <= (int64_t)p.max_blocks * kBlockTokens;
+    if (report && (!q_ok || !c_ok))
+        flag_error(p.dev_status, PA_DEV_BAD_CONTEXT_BIT);
+    s.ctx = c_ok ? ctx : 0;
+    s.q0 = q_ok ? q0 : 0;
+    s.nq = q_ok ? q1 - q0 : 0;
+    s.tiles = (int32_t)(((int64_t)s.ctx + kRows - 1) / kRows);
+    s.halves = (int32_t)(((int64_t)s.nq * p.g + kRows - 1) / kRows);
+    return s;
+}
+
+// A run of items of one unit that this CTA takes.
+struct Segment {
+    int kvh;
+    int halves;      // 1 or 2
+    int64_t row0;    // first packed row of the unit within (sequence, kv head)
+    int rows;        // live rows: 1 .. 256
+    int j0, j1;      // key tiles [j0, j1)
+    int64_t first_v; // the unit's first position on the line
+    bool leading;    // starts at this CTA's first position
+    bool whole;
+};
+
+struct Walk {
+    const CrossParams &p;
+    int64_t lo, hi, pos;
+    int b;
+    int64_t vb; // position of sequence b's first item
+    Seq s;
+
+    __device__ Walk(const CrossParams &p_, int64_t lo_, int64_t hi_, int b_, int64_t vb_)
+        : p(p_), lo(lo_), hi(hi_), pos(lo_), b(b_), vb(vb_)
+    {
+        if (pos < hi)
+            s = load_seq(p, b, false);
+    }
+
+    __device__ bool next(Segment &g)
+    {
+        while (pos < hi) {
+            int64_t c = s.cost(p.n_kv);
+            while (pos >= vb + c) { // (pos is below the line's end, so b stays in range)
+                vb += c;
+                s = load_seq(p, ++b, false);
+                c = s.cost(p.n_kv);
+            }
+            const int64_t head = (int64_t)s.tiles * s.halves;
+            int64_t r = pos - vb;
+            g.kvh = (int)div_small(r, head);
+            r -= g.kvh * head;
+            const int64_t pair = 2 * (int64_t)s.tiles;
+            const int64_t qt = div_small(r, pair);
+            const int64_t off = r - qt * pair;
+            g.halves = (int)min((int64_t)2, s.halves - 2 * qt);
+            g.first_v = pos - off;
+            const int64_t end = g.first_v + (int64_t)s.tiles * g.halves;
+            // an item belongs to the CTA that has its first position
+            g.j0 = (int)((off + g.halves - 1) / g.halves);
+            g.j1 = hi >= end ? s.tiles : (int)((hi - g.first_v + g.halves - 1) / g.halves);
+            g.leading = pos == lo;
+            pos = end;
+            if (g.j0 >= g.j1)
+                continue;
+            g.row0 = qt * kUnitRows;
+            g.rows = (int)min((int64_t)kUnitRows, (int64_t)s.nq * p.g - g.row0);
+            g.whole = g.j0 == 0 && g.j1 == s.tiles;
+            return true;
+        }
+        return false;
+    }
+};
+
+template <int D, int KIND>
+struct Smem {
+    static constexpr int TILE = kRows * D * 2; // one Q half, K tile or V tile in bf16
+    static constexpr int SLOTS = D == 128 ? 4 : 8;
+    static constexpr int kOffRing = 2 * TILE;
+    static constexpr int kOffScales = kOffRing + SLOTS * TILE; // [ring][K, V][128] fp32
+    static constexpr int kScaleBytes = KIND ? kScaleRing * 2 * kRows * 4 : 0;
+    static constexpr int kOffBars = kOffScales + kScaleBytes;
+    static constexpr int kBars = 2 + 2 * SLOTS + 6 + 1;
+    static constexpr int kOffMisc = kOffBars + (kBars * 8 + 15) / 16 * 16; // 64 int32
+    static constexpr int kBytes = 1024 + kOffMisc + 256;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tmap, int32_t x,
+                                            int32_t y, int32_t z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_stream_128(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two INT8 codes (bytes SEL picks, zero-extended to 16 bits) as bf16, exactly:
+// 0x4300 | low 7 bits is 128 + those bits, 0x4300 | sign bit is 128 or 256.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t code8_bf2(uint32_t x)
+{
+    const uint32_t w = __byte_perm(x, 0, SEL);
+    return sub_bf16x2((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0x43004300u);
+}
+
+// The two INT4 codes of byte K of the word whose low nibbles are a and high
+// nibbles b, offset by 8: 0x4300 | n is 128 + n, and 0x4308 is 136.
+template <int K>
+__device__ __forceinline__ uint32_t code4_bf2(uint32_t a, uint32_t b)
+{
+    const uint32_t t = __byte_perm(a, b, K | (K << 4) | ((4 + K) << 8) | ((4 + K) << 12));
+    return sub_bf16x2((t & 0x000f000fu) | 0x43004300u, 0x43084308u);
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+             const __grid_constant__ CUtensorMap tmV, const CrossParams p)
+{
+    using L = Smem<D, KIND>;
+    constexpr int SLOTS = L::SLOTS, TILE = L::TILE, HALVES = D / 64;
+    constexpr int COL = TILE / HALVES; // bytes of one 64-element column of a tile
+    constexpr int REC = D + 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t ring = sbase + L::kOffRing;
+    const uint32_t bars = sbase + L::kOffBars;
+    const uint32_t q_full = bars, q_empty = bars + 8, kv_full = bars + 16,
+                   kv_empty = kv_full + 8 * SLOTS, s_full = kv_empty + 8 * SLOTS,
+                   p_full = s_full + 16, o_full = p_full + 16, drained = o_full + 16;
+    // misc: [0] tensor memory base, [1] merge flag, [2..3] start sequence and
+    // position, [8..] bad-block masks per slot, [16..17] per half, [24..] scan
+    int32_t *misc = reinterpret_cast<int32_t *>(smem + L::kOffMisc);
+    volatile int32_t *slot_mask = misc + 8;
+    volatile int32_t *half_mask = misc + 16;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_h = p.n_kv * p.g;
+
+    // ---- this CTA's range of the line
+    int64_t total;
+    {
+        const int per = (p.num_seqs + kThreads - 1) / kThreads;
+        const int b0 = min(tid * per, p.num_seqs), b1 = min(b0 + per, p.num_seqs);
+        int64_t sum = 0;
+        for (int b = b0; b < b1; ++b)
+            sum += load_seq(p, b, blockIdx.x == 0).cost(p.n_kv);
+        int64_t x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        int64_t *wsum = reinterpret_cast<int64_t *>(misc + 24);
+        if (lane == 31)
+            wsum[warp] = x;
+        __syncthreads();
+        int64_t before = x - sum;
+        total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            before += w < warp ? wsum[w] : 0;
+            total += wsum[w];
+        }
+        if (total > 0) {
+            // at least two positions per CTA: each then owns an item
+            const int64_t G = max((int64_t)1, plan_ctas(p.num_ctas, total / 2));
+            const int64_t lo = plan_lo(blockIdx.x, total, G);
+            if (blockIdx.x < G && lo >= before && lo < before + sum) {
+                int b = b0;
+                int64_t v = before;
+                for (;; ++b) { // the sequence that holds position lo (there is one)
+                    const int64_t c = load_seq(p, b, false).cost(p.n_kv);
+                    if (lo < v + c)
+                        break;
+                    v += c;
+                }
+                misc[2] = b;
+                *reinterpret_cast<int64_t *>(misc + 4) = v;
+            }
+        }
+    }
+    // sequences without keys: zero rows
+    for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
+        const Seq s = load_seq(p, b, false);
+        if (s.nq > 0 && s.tiles == 0) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)s.q0 * n_h * D);
+            const int64_t n = (int64_t)s.nq * n_h * (D / 8);
+            for (int64_t i = tid; i < n; i += kThreads)
+                dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    const int64_t G = max((int64_t)1, plan_ctas(p.num_ctas, total / 2));
+    if (total == 0 || blockIdx.x >= G)
+        return;
+    const int64_t lo = plan_lo(blockIdx.x, total, G), hi = plan_lo(blockIdx.x + 1, total, G);
+
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(kv_full + 8 * s, KIND ? kLoaders : 1);
+            mbar_init(kv_empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 2); // the matrix instructions and the mask
+            mbar_init(p_full + 8 * i, kRows);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        mbar_init(drained, 1);
+        fence_barrier_init();
+    }
+    if (warp == 8)
+        tmem_alloc(smem_u32(misc), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)misc[0];
+    Walk walk(p, lo, hi, misc[2], *reinterpret_cast<int64_t *>(misc + 4));
+    Segment g;
+    bool dead = false; // a wait gave up: no more waits, no more copies or products
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, parity & 1u))) {
+            dead = true;
+            if (lane == 0)
+                flag_error(p.dev_status, PA_DEV_TIMEOUT_BIT);
+        }
+        return !dead;
+    };
+
+    if (warp < 8) {
+        // ================================================================ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int half = warp >> 2;
+        const int r = half * kRows + (tid & (kRows - 1)); // row within the unit
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21; // lane base of this warp, bits 16..
+        const uint32_t tS = tmem + lanes + half * 128, tO = tmem + lanes + 256 + half * 128;
+        const float *scales = reinterpret_cast<const float *>(smem + L::kOffScales);
+        uint32_t n_s = 0;     // tiles of this half so far
+        uint32_t n_tile = 0;  // tiles of this CTA so far (the scale ring's index)
+        while (walk.next(g)) {
+            const int ctx = walk.s.ctx;
+            float m = -INFINITY, l = 0.f;
+            const bool mine = half < g.halves;
+            for (int j = g.j0; mine && j < g.j1; ++j, ++n_s) {
+                if (!wait(s_full + 8 * half, n_s))
+                    break;
+                tc_fence_after();
+                const int bad = half_mask[half];
+                const int valid = min(ctx - j * kRows, kRows);
+                float s[kRows];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(tS + 32 * c, s + 32 * c);
+                tmem_wait_ld();
+                tmem_landed<kRows>(s);
+                // scores in the log2 domain = s * mul
+                float mul = p.scale_log2;
+                const float *sk = scales + ((n_tile + (uint32_t)(j - g.j0)) % kScaleRing) * 2 * kRows;
+                if constexpr (KIND != 0) {
+#pragma unroll
+                    for (int c = 0; c < kRows; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sk + c);
+                        s[c] *= f.x;
+                        s[c + 1] *= f.y;
+                        s[c + 2] *= f.z;
+                        s[c + 3] *= f.w;
+                    }
+                    mul = 1.f;
+                }
+                if (valid < kRows || bad) {
+#pragma unroll
+                    for (int c = 0; c < kRows; ++c)
+                        s[c] = c < valid && !((bad >> (c / kBlockTokens)) & 1) ? s[c] * mul
+                                                                               : -INFINITY;
+                    mul = 1.f;
+                }
+                float mx[4];
+                if (mul >= 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = s[e];
+#pragma unroll
+                    for (int c = 4; c < kRows; ++c)
+                        mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                    mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = s[e];
+#pragma unroll
+                    for (int c = 4; c < kRows; ++c)
+                        mx[c & 3] = fminf(mx[c & 3], s[c]);
+                    mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * mul;
+                }
+                if (j == g.j0) {
+                    m = mx[0];
+                } else {
+                    const bool up = mx[0] > m + kMoveLog2;
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float a = up ? fast_exp2(m - mx[0]) : 1.f;
+                        m = up ? mx[0] : m;
+                        l *= a;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(tO + c, o);
+                            tmem_wait_ld();
+                            tmem_landed<32>(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] *= a;
+                            tmem_st32(tO + c, reinterpret_cast<const uint32_t *>(o));
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float *sv = sk + kRows;
+#pragma unroll
+                for (int c = 0; c < kRows; c += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        float x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[i] = fast_exp2(fmaf(s[c + e + i], mul, -base));
+                            sum[i] += x[i];
+                        }
+                        if constexpr (KIND != 0) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sv + c + e);
+                            x[0] *= f.x;
+                            x[1] *= f.y;
+                            x[2] *= f.z;
+                            x[3] *= f.w;
+                        }
+                        w[e / 2] = pack_bf16x2(x[0], x[1]);
+                        w[e / 2 + 1] = pack_bf16x2(x[2], x[3]);
+                    }
+                    tmem_st32(tS + c / 2, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + 8 * half);
+            }
+            n_tile += (uint32_t)(g.j1 - g.j0);
+            // ---- the half's output, or its record
+            const bool live = mine && r < g.rows;
+            const int64_t row = g.row0 + r; // packed row of (sequence, kv head)
+            if (mine) {
+                wait(o_full + 8 * half, n_s - 1);
+                tc_fence_after();
+                const int64_t t = row / p.g, h = row - t * p.g;
+                __nv_bfloat16 *o_row =
+                    p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D;
+                float *rec = p.records +
+                             (((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1)) * kUnitRows + r) * REC;
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll 1
+                for (int c = 0; !dead && c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(tO + c, o);
+                    tmem_wait_ld();
+                    tmem_landed<32>(o);
+                    if (live && g.whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(o_row + c + e) = make_uint4(
+                                pack_bf16x2(o[e] * inv, o[e + 1] * inv),
+                                pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                                pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            *reinterpret_cast<float2 *>(rec + 2 + c + e) =
+                                make_float2(o[e], o[e + 1]);
+                    }
+                }
+                if (live && !g.whole) // (a sum that is not a number must not be skipped for its base)
+                    *reinterpret_cast<float2 *>(rec) = make_float2(l != l ? 0.f : m, l);
+                tc_fence_before(); // (the next p_full orders these reads before the next products)
+            }
+            if (g.whole)
+                continue;
+            // ---- a cut unit: the last CTA to arrive merges its records
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const int64_t c_first = plan_owner(g.first_v, total, G);
+            const int64_t last_v = g.first_v + (int64_t)(walk.s.tiles - 1) * g.halves;
+            const int nseg = (int)(plan_owner(last_v, total, G) - c_first + 1);
+            if (tid == 0) {
+                const int last = atomic_add_acq_rel_gpu(p.counters + c_first, 1) == nseg - 1;
+                if (last)
+                    p.counters[c_first] = 0; // every arrival is in: ready for the next call
+                misc[1] = last;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (!misc[1])
+                continue;
+            const int slot = g.first_v == plan_lo(c_first, total, G) ? 0 : 1;
+            const float *first = p.records + ((c_first * 2 + slot) * kUnitRows) * REC;
+            const float *rest = p.records + ((c_first + 1) * 2 * kUnitRows) * REC;
+            for (int i = tid; i < g.rows * (D / 4); i += 2 * kRows) {
+                const int rr = i / (D / 4), d0 = i % (D / 4) * 4;
+                RunState<4> st;
+                st.clear();
+                fold_rows<4, 1>(st, first + (int64_t)rr * REC, 0, 1, d0);
+                fold_rows<4, 4>(st, rest + (int64_t)rr * REC, (size_t)2 * kUnitRows * REC, nseg - 1,
+                                d0);
+                const float inv = st.L > 0.f || st.L != st.L ? 1.f / st.L : 0.f;
+                const int64_t pr = g.row0 + rr, t = pr / p.g, h = pr - t * p.g;
+                *reinterpret_cast<uint2 *>(p.out +
+                                           ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D + d0) =
+                    make_uint2(pack_bf16x2(st.O[0] * inv, st.O[1] * inv),
+                               pack_bf16x2(st.O[2] * inv, st.O[3] * inv));
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 8) {
+            // ======================================================== matrix instructions
+            constexpr uint32_t iS = tc_idesc_bf16(kRows, kRows, false);
+            constexpr uint32_t iO = tc_idesc_bf16(kRows, D, true);
+            uint32_t n_q = 0, n_kv = 0; // segments, ring slots consumed
+            uint32_t n_p[2] = {0, 0};   // products with V issued per half
+            auto slot_of = [&](uint32_t n) { return n % SLOTS; };
+            auto wait_slot = [&](uint32_t n) { return wait(kv_full + 8 * slot_of(n), n / SLOTS); };
+            // scores of one half: Q K^T. The half's previous P V must be done: it reads P
+            // where the scores go.
+            auto scores = [&](int i, uint32_t slot) {
+                if (n_p[i] && !wait(o_full + 8 * i, n_p[i] - 1))
+                    return;
+                tc_fence_after();
+                if (lane == 0) {
+                    half_mask[i] = slot_mask[slot];
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * COL + (kk % 4) * 32;
+                        tc_mma_ss(tmem + i * 128, tc_desc(sbase + i * TILE + off, 16),
+                                  tc_desc(ring + slot * TILE + off, 16), iS, kk > 0);
+                    }
+                    tc_commit(s_full + 8 * i);
+                    mbar_arrive(s_full + 8 * i);
+                }
+            };
+            while (walk.next(g)) {
+                const int n = g.j1 - g.j0, ctx = walk.s.ctx;
+                if (!wait(q_full, n_q) || !wait_slot(n_kv))
+                    break;
+                for (int i = 0; i < g.halves; ++i)
+                    scores(i, slot_of(n_kv));
+                if (dead)
+                    break;
+                if (lane == 0) {
+                    tc_commit(kv_empty + 8 * slot_of(n_kv));
+                    if (n == 1)
+                        tc_commit(q_empty);
+                }
+                ++n_kv;
+                for (int jj = 0; jj < n && !dead; ++jj) {
+                    const uint32_t vs = n_kv, ks = n_kv + 1;
+                    if (!wait_slot(vs))
+                        break;
+                    const uint32_t v_at = ring + slot_of(vs) * TILE;
+                    const int tail = ctx % kBlockTokens;
+                    if (KIND == 0 && tail && g.j0 + jj == walk.s.tiles - 1) {
+                        // rows behind the context may hold anything: 0 * NaN is NaN, so zero them
+                        const int r0 = ctx - (g.j0 + jj) * kRows;
+                        const int rows = kBlockTokens - tail;
+                        for (int i = lane; i < rows * (D / 8); i += 32) {
+                            const int rr = r0 + i / (D / 8), c = i % (D / 8);
+                            sts128(v_at + (c / 8) * COL + rr * 128 + (c % 8) * 16, 0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    for (int i = 0; i < g.halves && !dead; ++i) {
+                        if (!wait(p_full + 8 * i, n_p[i]))
+                            break;
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int kk = 0; kk < kRows / 16; ++kk)
+                                tc_mma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * kk,
+                                          tc_desc(v_at + kk * 2048, COL), iO, jj > 0 || kk > 0);
+                            tc_commit(o_full + 8 * i);
+                            if (i == g.halves - 1)
+                                tc_commit(kv_empty + 8 * slot_of(vs));
+                        }
+                        ++n_p[i];
+                        if (jj + 1 < n) {
+                            if (i == 0 && !wait_slot(ks))
+                                break;
+                            scores(i, slot_of(ks));
+                            if (dead)
+                                break;
+                            if (i == g.halves - 1 && lane == 0) {
+                                tc_commit(kv_empty + 8 * slot_of(ks));
+                                if (jj + 2 == n)
+                                    tc_commit(q_empty);
+                            }
+                        }
+                    }
+                    n_kv += jj + 1 < n ? 2 : 1;
+                }
+                if (dead)
+                    break;
+                ++n_q;
+            }
+            if (dead) { // let what was issued finish (bounded) before the memory goes
+                if (lane == 0)
+                    tc_commit(drained);
+                mbar_wait(drained, 0);
+            }
+        } else if (KIND != 0 || warp == 9) {
+            // ============================================================== copies
+            uint32_t n_q = 0, n_kv = 0, n_tile = 0;
+            auto load_q = [&]() {
+                if (!wait(q_empty, n_q + 1))
+                    return;
+                if (warp == 9 && lane == 0) {
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(g.halves * TILE));
+                    const int32_t t0 = (int32_t)(walk.s.q0 + g.row0 / p.g);
+                    for (int i = 0; i < g.halves; ++i)
+                        for (int c = 0; c < HALVES; ++c)
+                            tma_load_3d(sbase + i * TILE + c * COL, &tmQ, c * 64, g.kvh * p.g,
+                                        t0 + i * (kRows / p.g), q_full);
+                }
+                __syncwarp();
+                ++n_q;
+            };
+            while (walk.next(g) && !dead) {
+                const int ctx = walk.s.ctx;
+                const int nblk = (int)(((int64_t)ctx + kBlockTokens - 1) / kBlockTokens);
+                const int32_t *table = p.block_tables + (int64_t)walk.b * p.max_blocks;
+                for (int j = g.j0; j < g.j1; ++j, ++n_tile) {
+                    // lanes 0-7 (and their copies): the tile's eight blocks
+                    const int blk = j * kTileBlocks + (lane & 7);
+                    const int32_t phys = blk < nblk ? __ldg(table + blk) : -1;
+                    const bool ok = phys >= 0 && phys < p.num_blocks;
+                    const uint32_t bad =
+                        __ballot_sync(0xffffffffu, blk < nblk && !ok) & 0xffu;
+                    if (bad && lane == 0)
+                        flag_error(p.dev_status, PA_DEV_BAD_BLOCK_BIT);
+                    const int32_t prow = ok ? phys * p.n_kv + g.kvh : -1; // (block, head) tile
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++n_kv) {
+                        const uint32_t slot = n_kv % SLOTS;
+                        if (!wait(kv_empty + 8 * slot, n_kv / SLOTS + 1))
+                            break;
+                        const uint32_t full = kv_full + 8 * slot, dst = ring + slot * TILE;
+                        if (warp == 9 && lane == 0)
+                            slot_mask[slot] = (int32_t)bad;
+                        if constexpr (KIND == 0) {
+                            // absent and bad blocks: a box outside the pool arrives as zeros
+                            const int32_t y =
+                                ok ? prow * kBlockTokens
+                                   : (int32_t)(p.num_blocks * p.n_kv * kBlockTokens);
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(full, TILE);
+                            __syncwarp();
+                            if (lane < kTileBlocks * HALVES)
+                                tma_load_2d(dst + (lane >> 3) * COL + (lane & 7) * 2048,
+                                            kv ? &tmV : &tmK, (lane >> 3) * 64, y, full,
+                                            l2_policy_evict_normal());
+                            __syncwarp();
+                        } else {
+                            constexpr int ROWB = KIND == 1 ? D : D / 2;
+                            constexpr int CPR = ROWB / 16; // 16-byte chunks per row
+                            constexpr int CHUNKS = kRows * CPR;
+                            constexpr int PER = (CHUNKS + kLoaders - 1) / kLoaders;
+                            constexpr int BATCH = 6;
+                            const int t = tid - 9 * 32;
+                            const uint8_t *pool =
+                                static_cast<const uint8_t *>(kv ? p.v_cache : p.k_cache);
+                            if (kv == 0) { // the tile's scales, both kinds
+                                float *sc = reinterpret_cast<float *>(smem + L::kOffScales) +
+                                            (n_tile % kScaleRing) * 2 * kRows;
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int r = t + e * kLoaders;
+                                    const int32_t pr = __shfl_sync(0xffffffffu, prow, (r >> 4) & 7);
+                                    if (r < kRows) {
+                                        const bool in = pr >= 0 && j * kRows + r < ctx;
+                                        const int64_t at = (int64_t)pr * kBlockTokens + (r & 15);
+                                        sc[r] = in ? __ldg(p.k_scale + at) * p.scale_log2 : 0.f;
+                                        sc[kRows + r] = in ? __ldg(p.v_scale + at) : 0.f;
+                                    }
+                                }
+                            }
+#pragma unroll 1
+                            for (int e0 = 0; e0 < PER; e0 += BATCH) {
+                                uint4 x[BATCH];
+#pragma unroll
+                                for (int e = 0; e < BATCH; ++e) {
+                                    const int c = (e0 + e) * kLoaders + t, r = c / CPR;
+                                    const int32_t pr = __shfl_sync(0xffffffffu, prow, (r >> 4) & 7);
+                                    x[e] = make_uint4(0, 0, 0, 0);
+                                    if (c < CHUNKS && pr >= 0 && j * kRows + r < ctx)
+                                        x[e] = ld_stream_128(reinterpret_cast<const uint4 *>(pool) +
+                                                             (int64_t)pr * (kBlockTokens * CPR) +
+                                                             (r & 15) * CPR + c % CPR);
+                                }
+#pragma unroll
+                                for (int e = 0; e < BATCH; ++e) {
+                                    const int c = (e0 + e) * kLoaders + t, r = c / CPR;
+                                    if (c >= CHUNKS)
+                                        continue;
+                                    // first 16-byte chunk of 8 bf16 that this one becomes
+                                    const int o = c % CPR * (KIND == 1 ? 2 : 4);
+                                    auto put = [&](int i, uint32_t a, uint32_t b, uint32_t cc,
+                                                   uint32_t d) {
+                                        const int oc = o + i;
+                                        sts128(dst + (oc / 8) * COL + r * 128 +
+                                                   (((oc % 8) ^ (r & 7)) << 4),
+                                               a, b, cc, d);
+                                    };
+                                    const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+                                    if constexpr (KIND == 1) {
+#pragma unroll
+                                        for (int i = 0; i < 2; ++i)
+                                            put(i, code8_bf2<0x4140>(w[2 * i]),
+                                                code8_bf2<0x4342>(w[2 * i]),
+                                                code8_bf2<0x4140>(w[2 * i + 1]),
+                                                code8_bf2<0x4342>(w[2 * i + 1]));
+                                    } else {
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
+                                            put(i, code4_bf2<0>(a, b), code4_bf2<1>(a, b),
+                                                code4_bf2<2>(a, b), code4_bf2<3>(a, b));
+                                        }
+                                    }
+                                }
+                            }
+                            fence_proxy_async_smem();
+                            mbar_arrive(full);
+                        }
+                    }
+                    if (dead)
+                        break;
+                    if (j == g.j0)
+                        load_q();
+                }
+            }
+            if (KIND == 0 && dead) { // copies in flight land (bounded) before the memory goes
+                for (uint32_t n = n_kv > SLOTS ? n_kv - SLOTS : 0; n < n_kv; ++n)
+                    mbar_wait(kv_full + 8 * (n % SLOTS), (n / SLOTS) & 1u);
+            }
+            if (dead && n_q)
+                mbar_wait(q_full, (n_q - 1) & 1u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8)
+        tmem_dealloc(tmem, 512);
+}
+
+template <int D, int KIND>
+cudaError_t launch_of(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                      const CrossParams &p, cudaStream_t stream)
+{
+    constexpr int bytes = Smem<D, KIND>::kBytes;
+    static_assert(bytes <= 232448 && bytes > 116 * 1024, "one CTA per SM");
+    const cudaError_t e = cudaFuncSetAttribute(
+        cross_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess)
+        return e;
+    cross_kernel<D, KIND><<<p.num_ctas, kThreads, bytes, stream>>>(tq, tk, tv, p);
+    return cudaGetLastError();
+}
+
+size_t counter_bytes(int num_ctas) { return ((size_t)num_ctas * 4 + 255) / 256 * 256; }
+
+} // namespace
+
+size_t cross_workspace_bytes(int d_h, int num_ctas)
+{
+    return counter_bytes(num_ctas) + (size_t)num_ctas * 2 * kUnitRows * (d_h + 2) * sizeof(float);
+}
+
+cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                         const CrossArgs &a, cudaStream_t stream)
+{
+    CrossParams p;
+    p.k_cache = a.k_cache;
+    p.v_cache = a.v_cache;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.cu_q = a.cu_q;
+    p.block_tables = a.block_tables;
+    p.context_lens = a.context_lens;
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.counters = static_cast<int32_t *>(a.workspace);
+    p.records = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) +
+                                          counter_bytes(a.num_ctas));
+    p.dev_status = a.dev_status;
+    p.num_q = a.num_q;
+    p.num_blocks = a.num_blocks;
+    p.num_seqs = a.num_seqs;
+    p.n_kv = a.n_kv;
+    p.g = a.g;
+    p.max_blocks = a.max_blocks;
+    p.num_ctas = a.num_ctas;
+    p.scale_log2 = a.scale_log2;
+    const int kind = a.kind;
+    if (a.d_h == 128)
+        return kind == 0   ? launch_of<128, 0>(tq, tk, tv, p, stream)
+               : kind == 1 ? launch_of<128, 1>(tq, tk, tv, p, stream)
+                           : launch_of<128, 2>(tq, tk, tv, p, stream);
+    return kind == 0   ? launch_of<64, 0>(tq, tk, tv, p, stream)
+           : kind == 1 ? launch_of<64, 1>(tq, tk, tv, p, stream)
+                       : launch_of<64, 2>(tq, tk, tv, p, stream);
+}
+
+} // namespace pa

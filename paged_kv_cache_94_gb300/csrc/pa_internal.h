@@ -63,6 +63,21 @@ cudaError_t launch_mass(const float *scores, const float2 *ml, const int32_t *co
                         const float *mass, float *mass_out, int num_seqs, int n_kv, int g,
                         int max_blocks, int sms, cudaStream_t stream);
 
+// Cross attention (pa_cross.cu).
+struct CrossArgs {
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *cu_q, *block_tables, *context_lens;
+    void *out, *workspace;
+    int32_t *dev_status;
+    int64_t num_q, num_blocks;
+    int num_seqs, n_kv, g, d_h, kind, max_blocks, num_ctas;
+    float scale_log2;
+};
+size_t cross_workspace_bytes(int d_h, int num_ctas);
+cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                         const CrossArgs &a, cudaStream_t stream);
+
 // Eviction by accumulated attention weight (pa_evict.cu).
 cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t *context_lens,
                                 int num_seqs, int n_kv, int budget, int recent, int32_t *keep,

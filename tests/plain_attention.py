@@ -48,3 +48,14 @@ def choose(mass, n, budget, recent):
     # (sorted is stable: equal masses stay in index order; NaN among -inf is put last)
     nan_last = [j for j in rest if not np.isnan(mass[j])] + [j for j in rest if np.isnan(mass[j])]
     return sorted(nan_last[:k - r]) + list(range(n - r, n))
+
+
+def gather_rows(pool, scale, table, n, head):
+    """cached_rows in one gather, for long contexts."""
+    blocks = table[:-(-n // 16)].long()
+    x = pool[blocks, head].reshape(-1, pool.shape[-1])[:n]
+    if pool.dtype == torch.uint8:
+        x = torch.stack([x & 15, x >> 4], -1).flatten(1).to(torch.int16)
+        x = torch.where(x > 7, x - 16, x)
+    x = x.double()
+    return x if scale is None else x * scale[blocks, head].reshape(-1)[:n, None].double()
