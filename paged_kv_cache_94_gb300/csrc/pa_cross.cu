@@ -36,6 +36,8 @@
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
 
+#include <type_traits>
+
 namespace pa {
 namespace {
 
@@ -163,7 +165,7 @@ struct Smem {
     static constexpr int kOffScales = kOffRing + SLOTS * TILE; // [ring][K, V][128] fp32
     static constexpr int kScaleBytes = KIND ? kScaleRing * 2 * kRows * 4 : 0;
     static constexpr int kOffBars = kOffScales + kScaleBytes;
-    static constexpr int kBars = 2 + 2 * SLOTS + 6 + 1;
+    static constexpr int kBars = 2 + 2 * SLOTS + 8 + 1;
     static constexpr int kOffMisc = kOffBars + (kBars * 8 + 15) / 16 * 16; // 64 int32
     static constexpr int kBytes = 1024 + kOffMisc + 256;
 };
@@ -201,6 +203,13 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Two INT8 codes (bytes SEL picks, zero-extended to 16 bits) as bf16, exactly:
 // 0x4300 | low 7 bits is 128 + those bits, 0x4300 | sign bit is 128 or 256.
 template <uint32_t SEL>
@@ -217,6 +226,17 @@ __device__ __forceinline__ uint32_t code4_bf2(uint32_t a, uint32_t b)
 {
     const uint32_t t = __byte_perm(a, b, K | (K << 4) | ((4 + K) << 8) | ((4 + K) << 12));
     return sub_bf16x2((t & 0x000f000fu) | 0x43004300u, 0x43084308u);
+}
+
+// mbar_wait with its slow path out of line: the common case, a barrier that is
+// ready or nearly so, stays a few instructions.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity)
+{
+    return mbar_wait(bar, parity);
+}
+__device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity)
+{
+    return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity);
 }
 
 template <int D, int KIND>
@@ -236,8 +256,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     const uint32_t bars = sbase + L::kOffBars;
     const uint32_t q_full = bars, q_empty = bars + 8, kv_full = bars + 16,
                    kv_empty = kv_full + 8 * SLOTS, s_full = kv_empty + 8 * SLOTS,
-                   p_full = s_full + 16, o_full = p_full + 16, drained = o_full + 16;
-    // misc: [0] tensor memory base, [1] merge flag, [2..3] start sequence and
+                   p_full = s_full + 16 /* [half][part] */, o_full = p_full + 32,
+                   drained = o_full + 16;
+    // misc: [0] tensor memory base (0), [1] merge flag, [2..3] start sequence and
     // position, [8..] bad-block masks per slot, [16..17] per half, [24..] scan
     int32_t *misc = reinterpret_cast<int32_t *>(smem + L::kOffMisc);
     volatile int32_t *slot_mask = misc + 8;
@@ -313,18 +334,19 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 2); // the matrix instructions and the mask
-            mbar_init(p_full + 8 * i, kRows);
+            mbar_init(p_full + 16 * i, kRows);
+            mbar_init(p_full + 16 * i + 8, kRows);
             mbar_init(o_full + 8 * i, 1);
         }
         mbar_init(drained, 1);
         fence_barrier_init();
     }
     if (warp == 8)
-        tmem_alloc(smem_u32(misc), 512);
+        tmem_alloc(smem_u32(misc), 512); // all of it: its base address is 0
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)misc[0];
+    constexpr uint32_t tmem = 0;
     Walk walk(p, lo, hi, misc[2], *reinterpret_cast<int64_t *>(misc + 4));
     Segment g;
     bool dead = false; // a wait gave up: no more waits, no more copies or products
@@ -377,38 +399,29 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     }
                     mul = 1.f;
                 }
-                if (valid < kRows || bad) {
+                if (valid < kRows || bad || mul < 0.f) {
 #pragma unroll
                     for (int c = 0; c < kRows; ++c)
                         s[c] = c < valid && !((bad >> (c / kBlockTokens)) & 1) ? s[c] * mul
                                                                                : -INFINITY;
                     mul = 1.f;
                 }
-                float mx[4];
-                if (mul >= 0.f) {
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c < kRows - 4; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mx[e] = s[e];
-#pragma unroll
-                    for (int c = 4; c < kRows; ++c)
-                        mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-                    mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = s[e];
-#pragma unroll
-                    for (int c = 4; c < kRows; ++c)
-                        mx[c & 3] = fminf(mx[c & 3], s[c]);
-                    mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * mul;
-                }
+                        mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+                const float top = mul * fmaxf(max3(mx[0], s[kRows - 4], s[kRows - 3]),
+                                              fmaxf(max3(mx[1], s[kRows - 2], s[kRows - 1]),
+                                                    fmaxf(mx[2], mx[3])));
                 if (j == g.j0) {
-                    m = mx[0];
+                    m = top;
                 } else {
-                    const bool up = mx[0] > m + kMoveLog2;
+                    const bool up = top > m + kMoveLog2;
                     if (__any_sync(0xffffffffu, up)) {
-                        const float a = up ? fast_exp2(m - mx[0]) : 1.f;
-                        m = up ? mx[0] : m;
+                        const float a = up ? fast_exp2(m - top) : 1.f;
+                        m = up ? top : m;
                         l *= a;
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -423,9 +436,24 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         }
                     }
                 }
+                const int tail = ctx % kBlockTokens;
+                if (KIND == 0 && tail && j == walk.s.tiles - 1) {
+                    // V rows behind the context may hold anything, and 0 * NaN is NaN: zero
+                    // them before this half's products (both halves write the same zeros)
+                    const uint32_t fill = 2 * (n_tile + (uint32_t)(j - g.j0)) + 1;
+                    const uint32_t v_at = ring + fill % SLOTS * TILE;
+                    if (wait(kv_full + 8 * (fill % SLOTS), fill / SLOTS))
+                        for (int i = tid & (kRows - 1); i < (kBlockTokens - tail) * (D / 8);
+                             i += kRows) {
+                            const int rr = valid + i / (D / 8), c = i % (D / 8);
+                            sts128(v_at + (c / 8) * COL + rr * 128 + (c % 8) * 16, 0, 0, 0, 0);
+                        }
+                    fence_proxy_async_smem();
+                }
                 const float base = m == -INFINITY ? 0.f : m;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 const float *sv = sk + kRows;
+                // the products of the first 64 keys start while the others' weights are formed
 #pragma unroll
                 for (int c = 0; c < kRows; c += 64) {
                     uint32_t w[32];
@@ -448,11 +476,11 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         w[e / 2 + 1] = pack_bf16x2(x[2], x[3]);
                     }
                     tmem_st32(tS + c / 2, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full + 16 * half + c / 8);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(p_full + 8 * half);
             }
             n_tile += (uint32_t)(g.j1 - g.j0);
             // ---- the half's output, or its record
@@ -530,106 +558,126 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 8) {
             // ======================================================== matrix instructions
-            constexpr uint32_t iS = tc_idesc_bf16(kRows, kRows, false);
-            constexpr uint32_t iO = tc_idesc_bf16(kRows, D, true);
-            uint32_t n_q = 0, n_kv = 0; // segments, ring slots consumed
-            uint32_t n_p[2] = {0, 0};   // products with V issued per half
-            auto slot_of = [&](uint32_t n) { return n % SLOTS; };
-            auto wait_slot = [&](uint32_t n) { return wait(kv_full + 8 * slot_of(n), n / SLOTS); };
-            // scores of one half: Q K^T. The half's previous P V must be done: it reads P
-            // where the scores go.
-            auto scores = [&](int i, uint32_t slot) {
-                if (n_p[i] && !wait(o_full + 8 * i, n_p[i] - 1))
-                    return;
-                tc_fence_after();
-                if (lane == 0) {
-                    half_mask[i] = slot_mask[slot];
+            // One thread runs the whole loop: a warp would pay a vote and a broadcast at each
+            // of its waits and operands, which come one after another. The halves take strict
+            // turns (P V, then the next scores, of half 0, then of half 1), which keeps
+            // one in its softmax while the other has the tensor cores; with a thread per half
+            // they fall into step and both wait for both.
+            if (elect_one()) {
+                constexpr uint32_t iS = tc_idesc_bf16(kRows, kRows, false);
+                constexpr uint32_t iO = tc_idesc_bf16(kRows, D, true);
+                constexpr uint64_t kHigh = tc_desc_high();
+                constexpr uint32_t kSlotDesc = TILE >> 4;
+                const uint32_t q_desc = (uint32_t)tc_desc(sbase, 16);
+                const uint32_t k_ring = (uint32_t)tc_desc(ring, 16);
+                const uint32_t v_ring = (uint32_t)tc_desc(ring, COL);
+                uint32_t n_q = 0;             // segments
+                uint32_t slot = 0, phase = 0; // ring position
+                uint32_t np0 = 0, np1 = 0;    // products with V issued per half
+                auto ready = [&](uint32_t bar, uint32_t parity) {
+                    if (!dead && !mbar_ready(bar, parity & 1u)) {
+                        dead = true;
+                        flag_error(p.dev_status, PA_DEV_TIMEOUT_BIT);
+                    }
+                    return !dead;
+                };
+                auto next_slot = [&]() {
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                };
+                // scores of half I against the K tile in slot ks: Q K^T. The half's previous
+                // P V must be done: it reads P where the scores go.
+                auto scores = [&](auto half, uint32_t np, uint32_t ks, bool release, bool last) {
+                    constexpr int I = decltype(half)::value;
+                    const uint64_t k_desc = kHigh | (k_ring + ks * kSlotDesc);
+                    if (np && !ready(o_full + 8 * I, np - 1))
+                        return;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * COL + (kk % 4) * 32;
-                        tc_mma_ss(tmem + i * 128, tc_desc(sbase + i * TILE + off, 16),
-                                  tc_desc(ring + slot * TILE + off, 16), iS, kk > 0);
+                        const uint32_t off = ((kk / 4) * COL + (kk % 4) * 32) >> 4;
+                        tc_mma_ss(I * 128, kHigh | (q_desc + I * kSlotDesc + off), k_desc + off, iS,
+                                  kk > 0);
                     }
-                    tc_commit(s_full + 8 * i);
-                    mbar_arrive(s_full + 8 * i);
-                }
-            };
-            while (walk.next(g)) {
-                const int n = g.j1 - g.j0, ctx = walk.s.ctx;
-                if (!wait(q_full, n_q) || !wait_slot(n_kv))
-                    break;
-                for (int i = 0; i < g.halves; ++i)
-                    scores(i, slot_of(n_kv));
-                if (dead)
-                    break;
-                if (lane == 0) {
-                    tc_commit(kv_empty + 8 * slot_of(n_kv));
-                    if (n == 1)
+                    tc_commit(s_full + 8 * I);
+                    half_mask[I] = slot_mask[ks];
+                    mbar_arrive(s_full + 8 * I);
+                    if (release)
+                        tc_commit(kv_empty + 8 * ks);
+                    if (last)
                         tc_commit(q_empty);
-                }
-                ++n_kv;
-                for (int jj = 0; jj < n && !dead; ++jj) {
-                    const uint32_t vs = n_kv, ks = n_kv + 1;
-                    if (!wait_slot(vs))
-                        break;
-                    const uint32_t v_at = ring + slot_of(vs) * TILE;
-                    const int tail = ctx % kBlockTokens;
-                    if (KIND == 0 && tail && g.j0 + jj == walk.s.tiles - 1) {
-                        // rows behind the context may hold anything: 0 * NaN is NaN, so zero them
-                        const int r0 = ctx - (g.j0 + jj) * kRows;
-                        const int rows = kBlockTokens - tail;
-                        for (int i = lane; i < rows * (D / 8); i += 32) {
-                            const int rr = r0 + i / (D / 8), c = i % (D / 8);
-                            sts128(v_at + (c / 8) * COL + rr * 128 + (c % 8) * 16, 0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    for (int i = 0; i < g.halves && !dead; ++i) {
-                        if (!wait(p_full + 8 * i, n_p[i]))
-                            break;
-                        tc_fence_after();
-                        if (lane == 0) {
+                };
+                // output of half I (+)= P V with the V tile in slot vs, in two parts
+                auto outputs = [&](auto half, uint32_t &np, uint32_t vs, uint32_t more,
+                                   bool release) {
+                    constexpr int I = decltype(half)::value;
+                    const uint64_t v_desc = kHigh | (v_ring + vs * kSlotDesc);
 #pragma unroll
-                            for (int kk = 0; kk < kRows / 16; ++kk)
-                                tc_mma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * kk,
-                                          tc_desc(v_at + kk * 2048, COL), iO, jj > 0 || kk > 0);
-                            tc_commit(o_full + 8 * i);
-                            if (i == g.halves - 1)
-                                tc_commit(kv_empty + 8 * slot_of(vs));
-                        }
-                        ++n_p[i];
-                        if (jj + 1 < n) {
-                            if (i == 0 && !wait_slot(ks))
-                                break;
-                            scores(i, slot_of(ks));
-                            if (dead)
-                                break;
-                            if (i == g.halves - 1 && lane == 0) {
-                                tc_commit(kv_empty + 8 * slot_of(ks));
-                                if (jj + 2 == n)
-                                    tc_commit(q_empty);
-                            }
-                        }
+                    for (int part = 0; part < 2; ++part) {
+                        if (!ready(p_full + 16 * I + 8 * part, np))
+                            return;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = part * 4; kk < part * 4 + 4; ++kk)
+                            tc_mma_ts(256 + I * 128, I * 128 + 8 * kk, v_desc + kk * (2048 >> 4), iO,
+                                      kk > 0 ? 1 : more);
                     }
-                    n_kv += jj + 1 < n ? 2 : 1;
+                    tc_commit(o_full + 8 * I);
+                    if (release)
+                        tc_commit(kv_empty + 8 * vs);
+                    ++np;
+                };
+                using H0 = std::integral_constant<int, 0>;
+                using H1 = std::integral_constant<int, 1>;
+                while (walk.next(g)) {
+                    const int n = g.j1 - g.j0;
+                    const bool two = g.halves == 2;
+                    if (!ready(q_full, n_q) || !ready(kv_full + 8 * slot, phase))
+                        break;
+                    scores(H0(), np0, slot, !two, !two && n == 1);
+                    if (two)
+                        scores(H1(), np1, slot, true, n == 1);
+                    next_slot();
+#pragma unroll 1
+                    for (int jj = 0; jj < n && !dead; ++jj) {
+                        const uint32_t vs = slot;
+                        if (!ready(kv_full + 8 * vs, phase))
+                            break;
+                        next_slot();
+                        const bool more_keys = jj + 1 < n, last = jj + 2 == n;
+                        outputs(H0(), np0, vs, jj > 0, !two);
+                        if (more_keys) {
+                            if (!ready(kv_full + 8 * slot, phase))
+                                break;
+                            scores(H0(), np0, slot, !two, !two && last);
+                        }
+                        if (two) {
+                            outputs(H1(), np1, vs, jj > 0, true);
+                            if (more_keys)
+                                scores(H1(), np1, slot, true, last);
+                        }
+                        if (more_keys)
+                            next_slot();
+                    }
+                    if (dead)
+                        break;
+                    ++n_q;
                 }
-                if (dead)
-                    break;
-                ++n_q;
-            }
-            if (dead) { // let what was issued finish (bounded) before the memory goes
-                if (lane == 0)
+                if (dead) { // let what was issued finish (bounded) before the memory goes
                     tc_commit(drained);
-                mbar_wait(drained, 0);
+                    mbar_wait(drained, 0);
+                }
             }
+            __syncwarp();
         } else if (KIND != 0 || warp == 9) {
             // ============================================================== copies
             uint32_t n_q = 0, n_kv = 0, n_tile = 0;
-            auto load_q = [&]() {
-                if (!wait(q_empty, n_q + 1))
+            auto load_q = [&]() { // (warp 9 alone: the barrier does not wait for the others)
+                if (warp != 9 || !wait(q_empty, n_q + 1))
                     return;
-                if (warp == 9 && lane == 0) {
+                if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, (uint32_t)(g.halves * TILE));
                     const int32_t t0 = (int32_t)(walk.s.q0 + g.row0 / p.g);
                     for (int i = 0; i < g.halves; ++i)
@@ -662,18 +710,27 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         const uint32_t full = kv_full + 8 * slot, dst = ring + slot * TILE;
                         if (warp == 9 && lane == 0)
                             slot_mask[slot] = (int32_t)bad;
+                        __syncwarp();
                         if constexpr (KIND == 0) {
                             // absent and bad blocks: a box outside the pool arrives as zeros
                             const int32_t y =
                                 ok ? prow * kBlockTokens
                                    : (int32_t)(p.num_blocks * p.n_kv * kBlockTokens);
-                            if (lane == 0)
-                                mbar_arrive_expect_tx(full, TILE);
-                            __syncwarp();
-                            if (lane < kTileBlocks * HALVES)
-                                tma_load_2d(dst + (lane >> 3) * COL + (lane & 7) * 2048,
-                                            kv ? &tmV : &tmK, (lane >> 3) * 64, y, full,
-                                            l2_policy_evict_normal());
+                            int32_t ys[kTileBlocks];
+#pragma unroll
+                            for (int i = 0; i < kTileBlocks; ++i)
+                                ys[i] = __shfl_sync(0xffffffffu, y, i);
+                            const CUtensorMap *tm = kv ? &tmV : &tmK;
+                            const uint32_t d0 = warp_uniform(dst), f0 = warp_uniform(full);
+                            if (elect_one()) {
+                                const uint64_t pol = l2_policy_evict_normal();
+                                mbar_arrive_expect_tx(f0, TILE);
+#pragma unroll
+                                for (int i = 0; i < kTileBlocks; ++i)
+#pragma unroll
+                                    for (int c = 0; c < HALVES; ++c)
+                                        tma_load_2d(d0 + c * COL + i * 2048, tm, c * 64, ys[i], f0, pol);
+                            }
                             __syncwarp();
                         } else {
                             constexpr int ROWB = KIND == 1 ? D : D / 2;

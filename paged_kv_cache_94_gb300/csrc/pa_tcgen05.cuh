@@ -76,6 +76,25 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
                  : "memory");
 }
 
+// A value the whole warp agrees on, from lane 0: matrix instructions take their
+// operands from uniform registers, and moving each there from an ordinary one costs more
+// than the instruction's own issue.
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t x)
+{
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.b32 %0, 1, 0, p;\n\t}"
+                 : "=r"(yes));
+    return yes != 0;
+}
+
 // Shared-memory operand in the 128-byte swizzle, groups of eight rows 1024 bytes apart;
 // mn_stride: bytes between 64-element columns of an MN-major operand (unused
 // by a K-major one).
@@ -83,6 +102,12 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t mn_stride)
 {
     return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)((mn_stride >> 4) & 0x3fff) << 16 |
            (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Its upper word: the same for every operand (the lower one is the address and mn_stride).
+constexpr uint64_t tc_desc_high()
+{
+    return (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N, A K-major, B K- or MN-major.

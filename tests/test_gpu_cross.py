@@ -160,6 +160,19 @@ def test_value_ranges(kv, kind):
         check(out, q, cu, pool, bt, [n], scale)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
+def test_many_short_segments_per_cta(kv):
+    """Units of one or two key tiles, many to a CTA: the stages hand over at every tile."""
+    gen = torch.Generator().manual_seed(12)
+    q_lens = torch.randint(1, 300, (60,), generator=gen).tolist()
+    ctx = torch.randint(1, 400, (60,), generator=gen).tolist()
+    q, cu, pool, bt = case(kv, 128, 1, 4, q_lens, ctx, seed=12)
+    for num_ctas in (0, 5):
+        out, st = run(q, cu, pool, bt, ctx, 0.09, num_ctas=num_ctas)
+        assert st == 0
+        check(out, q, cu, pool, bt, ctx, 0.09)
+
+
 def test_single_queries_agree_with_the_decode():
     ctx = [700, 33, 4100, 128]
     q, cu, pool, bt = case("bf16", 128, 4, 2, [1] * 4, ctx, seed=7)
