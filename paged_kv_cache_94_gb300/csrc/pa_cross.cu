@@ -203,6 +203,33 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -361,7 +388,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 
     if (warp < 8) {
         // ================================================================ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp >> 2;
         const int r = half * kRows + (tid & (kRows - 1)); // row within the unit
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // lane base of this warp, bits 16..
@@ -392,10 +419,13 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll
                     for (int c = 0; c < kRows; c += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(sk + c);
-                        s[c] *= f.x;
-                        s[c + 1] *= f.y;
-                        s[c + 2] *= f.z;
-                        s[c + 3] *= f.w;
+                        const float2 a = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
+                        const float2 b =
+                            mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
+                        s[c] = a.x;
+                        s[c + 1] = a.y;
+                        s[c + 2] = b.x;
+                        s[c + 3] = b.y;
                     }
                     mul = 1.f;
                 }
@@ -451,7 +481,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     fence_proxy_async_smem();
                 }
                 const float base = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 mul_2 = make_float2(mul, mul), base_2 = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float *sv = sk + kRows;
                 // the products of the first 64 keys start while the others' weights are formed
 #pragma unroll
@@ -459,28 +490,29 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     uint32_t w[32];
 #pragma unroll
                     for (int e = 0; e < 64; e += 4) {
-                        float x[4];
+                        float2 x[2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            x[i] = fast_exp2(fmaf(s[c + e + i], mul, -base));
-                            sum[i] += x[i];
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = c + e + 2 * i;
+                            x[i] = fma2(make_float2(s[at], s[at + 1]), mul_2, base_2);
+                            x[i].x = fast_exp2(x[i].x);
+                            x[i].y = fast_exp2(x[i].y);
+                            sum[i] = add2(sum[i], x[i]);
                         }
                         if constexpr (KIND != 0) {
                             const float4 f = *reinterpret_cast<const float4 *>(sv + c + e);
-                            x[0] *= f.x;
-                            x[1] *= f.y;
-                            x[2] *= f.z;
-                            x[3] *= f.w;
+                            x[0] = mul2(x[0], make_float2(f.x, f.y));
+                            x[1] = mul2(x[1], make_float2(f.z, f.w));
                         }
-                        w[e / 2] = pack_bf16x2(x[0], x[1]);
-                        w[e / 2 + 1] = pack_bf16x2(x[2], x[3]);
+                        w[e / 2] = pack_bf16x2(x[0].x, x[0].y);
+                        w[e / 2 + 1] = pack_bf16x2(x[1].x, x[1].y);
                     }
                     tmem_st32(tS + c / 2, w);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(p_full + 16 * half + c / 8);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             n_tile += (uint32_t)(g.j1 - g.j0);
             // ---- the half's output, or its record
@@ -555,7 +587,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
             // ======================================================== matrix instructions
             // One thread runs the whole loop: a warp would pay a vote and a broadcast at each
@@ -581,17 +613,13 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     }
                     return !dead;
                 };
-                auto next_slot = [&]() {
-                    if (++slot == SLOTS) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
-                };
                 // scores of half I against the K tile in slot ks: Q K^T. The half's previous
                 // P V must be done: it reads P where the scores go.
                 auto scores = [&](auto half, uint32_t np, uint32_t ks, bool release, bool last) {
                     constexpr int I = decltype(half)::value;
                     const uint64_t k_desc = kHigh | (k_ring + ks * kSlotDesc);
+                    half_mask[I] = slot_mask[ks]; // (the softmax is done with the last one)
+                    mbar_arrive(s_full + 8 * I);
                     if (np && !ready(o_full + 8 * I, np - 1))
                         return;
                     tc_fence_after();
@@ -602,8 +630,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                   kk > 0);
                     }
                     tc_commit(s_full + 8 * I);
-                    half_mask[I] = slot_mask[ks];
-                    mbar_arrive(s_full + 8 * I);
                     if (release)
                         tc_commit(kv_empty + 8 * ks);
                     if (last)
@@ -631,35 +657,40 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 };
                 using H0 = std::integral_constant<int, 0>;
                 using H1 = std::integral_constant<int, 1>;
+                // the next ring slot, once it is filled
+                auto take = [&](uint32_t &at) {
+                    at = slot;
+                    const uint32_t parity = phase;
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                    return ready(kv_full + 8 * at, parity);
+                };
                 while (walk.next(g)) {
                     const int n = g.j1 - g.j0;
                     const bool two = g.halves == 2;
-                    if (!ready(q_full, n_q) || !ready(kv_full + 8 * slot, phase))
+                    uint32_t ks, vs;
+                    if (!ready(q_full, n_q) || !take(ks))
                         break;
-                    scores(H0(), np0, slot, !two, !two && n == 1);
-                    if (two)
-                        scores(H1(), np1, slot, true, n == 1);
-                    next_slot();
+                    scores(H0(), np0, ks, !two, !two && n == 1);
+                    if (!take(vs))
+                        break;
 #pragma unroll 1
                     for (int jj = 0; jj < n && !dead; ++jj) {
-                        const uint32_t vs = slot;
-                        if (!ready(kv_full + 8 * vs, phase))
-                            break;
-                        next_slot();
-                        const bool more_keys = jj + 1 < n, last = jj + 2 == n;
+                        const bool more = jj + 1 < n;
+                        if (two)
+                            scores(H1(), np1, ks, true, !more);
                         outputs(H0(), np0, vs, jj > 0, !two);
-                        if (more_keys) {
-                            if (!ready(kv_full + 8 * slot, phase))
+                        if (more) {
+                            if (!take(ks))
                                 break;
-                            scores(H0(), np0, slot, !two, !two && last);
+                            scores(H0(), np0, ks, !two, !two && jj + 2 == n);
                         }
-                        if (two) {
+                        if (two)
                             outputs(H1(), np1, vs, jj > 0, true);
-                            if (more_keys)
-                                scores(H1(), np1, slot, true, last);
-                        }
-                        if (more_keys)
-                            next_slot();
+                        if (more && !take(vs))
+                            break;
                     }
                     if (dead)
                         break;
