@@ -44,6 +44,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 128;       // query rows of a half, keys of a tile
 constexpr int kTileBlocks = kRows / kBlockTokens;
+constexpr int kPart = kRows / 2; // keys of one softmax step
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kLoaders = 96;     // INT8/INT4 loader threads
 constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
@@ -58,7 +59,7 @@ struct CrossParams {
     const int32_t *block_tables;
     const int32_t *context_lens;
     __nv_bfloat16 *out;
-    float *records;    // [num_ctas][2][256][D + 2]
+    float *records;    // [num_ctas][2], see record_floats
     int32_t *counters; // [num_ctas], zero between calls
     int32_t *dev_status;
     int64_t num_q;
@@ -157,6 +158,63 @@ struct Walk {
     }
 };
 
+// A record: O as float4 [d / 4][row], then (m, l) per row; coalesced for a thread per row.
+constexpr int record_floats(int d) { return kUnitRows * (d + 2); }
+
+// Log-sum-exp state of eight adjacent outputs of one row.
+struct MergeState {
+    float m, l, o[8];
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o[e] = 0.f;
+    }
+    // Outputs 8 d8 .. 8 d8 + 7 of row `row` of one or two (r1 not NULL) records.
+    template <int D>
+    __device__ __forceinline__ void fold(const float *r0, const float *r1, int row, int d8)
+    {
+        float2 ml[2];
+        float4 x[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float *r = k ? r1 : r0;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r) {
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(r + D * kUnitRows) + row);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    x[k][e] = __ldcg(reinterpret_cast<const float4 *>(r) +
+                                     (2 * d8 + e) * kUnitRows + row);
+            }
+        }
+        const float top = fmaxf(m, fmaxf(ml[0].x, ml[1].x));
+        if (top == -INFINITY)
+            return;
+        const float a = fast_exp2(m - top);
+        m = top;
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o[e] *= a;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float f = fast_exp2(ml[k].x - top);
+            l = fmaf(f, ml[k].y, l);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                o[4 * e] = fmaf(f, x[k][e].x, o[4 * e]);
+                o[4 * e + 1] = fmaf(f, x[k][e].y, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(f, x[k][e].z, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(f, x[k][e].w, o[4 * e + 3]);
+            }
+        }
+    }
+};
+
 template <int D, int KIND>
 struct Smem {
     static constexpr int TILE = kRows * D * 2; // one Q half, K tile or V tile in bf16
@@ -165,7 +223,7 @@ struct Smem {
     static constexpr int kOffScales = kOffRing + SLOTS * TILE; // [ring][K, V][128] fp32
     static constexpr int kScaleBytes = KIND ? kScaleRing * 2 * kRows * 4 : 0;
     static constexpr int kOffBars = kOffScales + kScaleBytes;
-    static constexpr int kBars = 2 + 2 * SLOTS + 8 + 1;
+    static constexpr int kBars = 2 + 2 * SLOTS + 10 + 1;
     static constexpr int kOffMisc = kOffBars + (kBars * 8 + 15) / 16 * 16; // 64 int32
     static constexpr int kBytes = 1024 + kOffMisc + 256;
 };
@@ -274,7 +332,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     using L = Smem<D, KIND>;
     constexpr int SLOTS = L::SLOTS, TILE = L::TILE, HALVES = D / 64;
     constexpr int COL = TILE / HALVES; // bytes of one 64-element column of a tile
-    constexpr int REC = D + 2;
+    constexpr int RECORD = record_floats(D);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -284,12 +342,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     const uint32_t q_full = bars, q_empty = bars + 8, kv_full = bars + 16,
                    kv_empty = kv_full + 8 * SLOTS, s_full = kv_empty + 8 * SLOTS,
                    p_full = s_full + 16 /* [half][part] */, o_full = p_full + 32,
-                   drained = o_full + 16;
+                   a_full = o_full + 16, drained = a_full + 16;
     // misc: [0] tensor memory base (0), [1] merge flag, [2..3] start sequence and
     // position, [8..] bad-block masks per slot, [16..17] per half, [24..] scan
     int32_t *misc = reinterpret_cast<int32_t *>(smem + L::kOffMisc);
     volatile int32_t *slot_mask = misc + 8;
     volatile int32_t *half_mask = misc + 16;
+
+    auto record = [&](int64_t i) { return p.records + i * RECORD; };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_h = p.n_kv * p.g;
@@ -364,6 +424,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             mbar_init(p_full + 16 * i, kRows);
             mbar_init(p_full + 16 * i + 8, kRows);
             mbar_init(o_full + 8 * i, 1);
+            mbar_init(a_full + 8 * i, 1);
         }
         mbar_init(drained, 1);
         fence_barrier_init();
@@ -407,65 +468,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const int bad = half_mask[half];
                 const int valid = min(ctx - j * kRows, kRows);
                 float s[kRows];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32(tS + 32 * c, s + 32 * c);
+                tmem_ld32(tS, s);
+                tmem_ld32(tS + 32, s + 32);
                 tmem_wait_ld();
-                tmem_landed<kRows>(s);
-                // scores in the log2 domain = s * mul
-                float mul = p.scale_log2;
-                const float *sk = scales + ((n_tile + (uint32_t)(j - g.j0)) % kScaleRing) * 2 * kRows;
-                if constexpr (KIND != 0) {
-#pragma unroll
-                    for (int c = 0; c < kRows; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sk + c);
-                        const float2 a = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
-                        const float2 b =
-                            mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
-                        s[c] = a.x;
-                        s[c + 1] = a.y;
-                        s[c + 2] = b.x;
-                        s[c + 3] = b.y;
-                    }
-                    mul = 1.f;
-                }
-                if (valid < kRows || bad || mul < 0.f) {
-#pragma unroll
-                    for (int c = 0; c < kRows; ++c)
-                        s[c] = c < valid && !((bad >> (c / kBlockTokens)) & 1) ? s[c] * mul
-                                                                               : -INFINITY;
-                    mul = 1.f;
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int c = 4; c < kRows - 4; c += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-                const float top = mul * fmaxf(max3(mx[0], s[kRows - 4], s[kRows - 3]),
-                                              fmaxf(max3(mx[1], s[kRows - 2], s[kRows - 1]),
-                                                    fmaxf(mx[2], mx[3])));
-                if (j == g.j0) {
-                    m = top;
-                } else {
-                    const bool up = top > m + kMoveLog2;
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float a = up ? fast_exp2(m - top) : 1.f;
-                        m = up ? top : m;
-                        l *= a;
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(tO + c, o);
-                            tmem_wait_ld();
-                            tmem_landed<32>(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] *= a;
-                            tmem_st32(tO + c, reinterpret_cast<const uint32_t *>(o));
-                        }
-                    }
-                }
+                tmem_landed<kPart>(s);
+                tmem_ld32(tS + 64, s + 64);
+                tmem_ld32(tS + 96, s + 96);
+                const float *sk =
+                    scales + ((n_tile + (uint32_t)(j - g.j0)) % kScaleRing) * 2 * kRows;
                 const int tail = ctx % kBlockTokens;
                 if (KIND == 0 && tail && j == walk.s.tiles - 1) {
                     // V rows behind the context may hold anything, and 0 * NaN is NaN: zero
@@ -480,39 +490,105 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         }
                     fence_proxy_async_smem();
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                const float2 mul_2 = make_float2(mul, mul), base_2 = make_float2(-base, -base);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                const float *sv = sk + kRows;
-                // the products of the first 64 keys start while the others' weights are formed
+                // The tile's two halves of 64 keys are two steps of the online softmax: the
+                // products of the first start while the weights of the second are formed.
 #pragma unroll
-                for (int c = 0; c < kRows; c += 64) {
+                for (int part = 0; part < 2; ++part) {
+                    const int c0 = part * kPart;
+                    if (part == 1) {
+                        tmem_wait_ld();
+                        tmem_landed<kPart>(s + kPart);
+                    }
+                    // scores in the log2 domain = s * mul
+                    float mul = p.scale_log2;
+                    if constexpr (KIND != 0) {
+#pragma unroll
+                        for (int c = c0; c < c0 + kPart; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sk + c);
+                            const float2 a =
+                                mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
+                            const float2 b =
+                                mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
+                            s[c] = a.x;
+                            s[c + 1] = a.y;
+                            s[c + 2] = b.x;
+                            s[c + 3] = b.y;
+                        }
+                        mul = 1.f;
+                    }
+                    if (valid < kRows || bad || mul < 0.f) {
+#pragma unroll
+                        for (int c = c0; c < c0 + kPart; ++c)
+                            s[c] = c < valid && !((bad >> (c / kBlockTokens)) & 1) ? s[c] * mul
+                                                                                   : -INFINITY;
+                        mul = 1.f;
+                    }
+                    float mx[4] = {s[c0], s[c0 + 1], s[c0 + 2], s[c0 + 3]};
+#pragma unroll
+                    for (int c = c0 + 4; c < c0 + kPart - 4; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+                    const float *end = s + c0 + kPart - 4;
+                    const float top = mul * fmaxf(max3(mx[0], end[0], end[1]),
+                                                  fmaxf(max3(mx[1], end[2], end[3]),
+                                                        fmaxf(mx[2], mx[3])));
+                    if (part == 0 && j == g.j0) {
+                        m = top;
+                    } else {
+                        const bool up = top > m + kMoveLog2;
+                        if (__any_sync(0xffffffffu, up)) {
+                            // O holds every earlier tile, and in the second step the first's
+                            // products, once they are done
+                            if (part == 1) {
+                                wait(a_full + 8 * half, n_s);
+                                tc_fence_after();
+                            }
+                            const float a = up ? fast_exp2(m - top) : 1.f;
+                            m = up ? top : m;
+                            l *= a;
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                tmem_ld32(tO + c, o);
+                                tmem_wait_ld();
+                                tmem_landed<32>(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] *= a;
+                                tmem_st32(tO + c, reinterpret_cast<const uint32_t *>(o));
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    const float2 mul_2 = make_float2(mul, mul), base_2 = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
+                    for (int e = 0; e < kPart; e += 4) {
                         float2 x[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int at = c + e + 2 * i;
+                            const int at = c0 + e + 2 * i;
                             x[i] = fma2(make_float2(s[at], s[at + 1]), mul_2, base_2);
                             x[i].x = fast_exp2(x[i].x);
                             x[i].y = fast_exp2(x[i].y);
                             sum[i] = add2(sum[i], x[i]);
                         }
                         if constexpr (KIND != 0) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sv + c + e);
+                            const float4 f = *reinterpret_cast<const float4 *>(sk + kRows + c0 + e);
                             x[0] = mul2(x[0], make_float2(f.x, f.y));
                             x[1] = mul2(x[1], make_float2(f.z, f.w));
                         }
                         w[e / 2] = pack_bf16x2(x[0].x, x[0].y);
                         w[e / 2 + 1] = pack_bf16x2(x[1].x, x[1].y);
                     }
-                    tmem_st32(tS + c / 2, w);
+                    tmem_st32(tS + c0 / 2, w);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(p_full + 16 * half + c / 8);
+                    mbar_arrive(p_full + 16 * half + 8 * part);
                 }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             n_tile += (uint32_t)(g.j1 - g.j0);
             // ---- the half's output, or its record
@@ -524,8 +600,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const int64_t t = row / p.g, h = row - t * p.g;
                 __nv_bfloat16 *o_row =
                     p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D;
-                float *rec = p.records +
-                             (((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1)) * kUnitRows + r) * REC;
+                float *rec = record((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1));
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll 1
                 for (int c = 0; !dead && c < D; c += 32) {
@@ -543,13 +618,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                 pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
                     } else if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            *reinterpret_cast<float2 *>(rec + 2 + c + e) =
-                                make_float2(o[e], o[e + 1]);
+                        for (int e = 0; e < 32; e += 4)
+                            reinterpret_cast<float4 *>(rec)[(c + e) / 4 * kUnitRows + r] =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
                 if (live && !g.whole) // (a sum that is not a number must not be skipped for its base)
-                    *reinterpret_cast<float2 *>(rec) = make_float2(l != l ? 0.f : m, l);
+                    reinterpret_cast<float2 *>(rec + D * kUnitRows)[r] =
+                        make_float2(l != l ? 0.f : m, l);
                 tc_fence_before(); // (the next p_full orders these reads before the next products)
             }
             if (g.whole)
@@ -569,21 +645,40 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             if (!misc[1])
                 continue;
             const int slot = g.first_v == plan_lo(c_first, total, G) ? 0 : 1;
-            const float *first = p.records + ((c_first * 2 + slot) * kUnitRows) * REC;
-            const float *rest = p.records + ((c_first + 1) * 2 * kUnitRows) * REC;
-            for (int i = tid; i < g.rows * (D / 4); i += 2 * kRows) {
-                const int rr = i / (D / 4), d0 = i % (D / 4) * 4;
-                RunState<4> st;
-                st.clear();
-                fold_rows<4, 1>(st, first + (int64_t)rr * REC, 0, 1, d0);
-                fold_rows<4, 4>(st, rest + (int64_t)rr * REC, (size_t)2 * kUnitRows * REC, nseg - 1,
-                                d0);
-                const float inv = st.L > 0.f || st.L != st.L ? 1.f / st.L : 0.f;
-                const int64_t pr = g.row0 + rr, t = pr / p.g, h = pr - t * p.g;
-                *reinterpret_cast<uint2 *>(p.out +
-                                           ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D + d0) =
-                    make_uint2(pack_bf16x2(st.O[0] * inv, st.O[1] * inv),
-                               pack_bf16x2(st.O[2] * inv, st.O[3] * inv));
+            // thread: eight outputs of a row at a time, adjacent rows in adjacent threads; two
+            // such pieces and up to two records are in flight together
+            const float *first = record(c_first * 2 + slot), *rest = record((c_first + 1) * 2);
+            const int pieces = g.rows * (D / 8);
+            for (int i0 = tid; i0 < pieces; i0 += 4 * kRows) {
+                MergeState st[2];
+                int rr[2], d8[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = min(i0 + e * 2 * kRows, pieces - 1);
+                    d8[e] = i / g.rows;
+                    rr[e] = i - d8[e] * g.rows;
+                    st[e].clear();
+                }
+                for (int q = 0; q < nseg; q += 2) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float *r0 = q == 0 ? first : rest + (int64_t)(q - 1) * 2 * RECORD;
+                        const float *r1 = q + 1 < nseg ? rest + (int64_t)q * 2 * RECORD : nullptr;
+                        st[e].template fold<D>(r0, r1, rr[e], d8[e]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float L = st[e].l, inv = L > 0.f || L != L ? 1.f / L : 0.f;
+                    const float *o = st[e].o;
+                    const int64_t pr = g.row0 + rr[e], t = pr / p.g, h = pr - t * p.g;
+                    *reinterpret_cast<uint4 *>(
+                        p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D + 8 * d8[e]) =
+                        make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv),
+                                   pack_bf16x2(o[2] * inv, o[3] * inv),
+                                   pack_bf16x2(o[4] * inv, o[5] * inv),
+                                   pack_bf16x2(o[6] * inv, o[7] * inv));
+                }
             }
         }
     } else {
@@ -649,6 +744,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         for (int kk = part * 4; kk < part * 4 + 4; ++kk)
                             tc_mma_ts(256 + I * 128, I * 128 + 8 * kk, v_desc + kk * (2048 >> 4), iO,
                                       kk > 0 ? 1 : more);
+                        if (part == 0)
+                            tc_commit(a_full + 8 * I);
                     }
                     tc_commit(o_full + 8 * I);
                     if (release)
@@ -877,7 +974,7 @@ size_t counter_bytes(int num_ctas) { return ((size_t)num_ctas * 4 + 255) / 256 *
 
 size_t cross_workspace_bytes(int d_h, int num_ctas)
 {
-    return counter_bytes(num_ctas) + (size_t)num_ctas * 2 * kUnitRows * (d_h + 2) * sizeof(float);
+    return counter_bytes(num_ctas) + (size_t)num_ctas * 2 * record_floats(d_h) * sizeof(float);
 }
 
 cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
