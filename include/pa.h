@@ -356,7 +356,7 @@ size_t pa_decode_mq_workspace_size(pa_geom geom, int32_t num_seqs, int32_t n_q,
  *   cu_q      int32 [num_seqs + 1] (device): offsets, not decreasing, within
  *             0 .. num_q; a sequence may have none. Rows of out that no sequence
  *             has (before cu_q[0], from cu_q[num_seqs] on) are left as they were.
- *   the pools, their scales (4-byte aligned), block_tables, context_lens, scale
+ *   the pools, their scales (16-byte aligned), block_tables, context_lens, scale
  *             as in pa_decode, for bf16, INT8 and INT4 pools; ctx_b == 0 gives
  *             zero rows
  *   workspace >= pa_cross_workspace_size(geom, num_ctas) bytes, 256-byte

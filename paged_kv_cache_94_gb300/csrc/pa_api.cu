@@ -809,7 +809,7 @@ pa_status pa_cross_attention(const void *q, int64_t num_q, const int32_t *cu_q,
         return PA_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
-        !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
+        !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
         return PA_ERR_ALIGNMENT;
     int dev, sms;
     if ((st = current_device(dev, sms)) != PA_OK)

@@ -17,14 +17,14 @@
 // by CTA borders leaves (m, l, O) records; the last CTA to finish it merges them
 // (log-sum-exp). No CTA waits for another.
 //
-// One CTA per SM, 12 warps:
+// One CTA per SM, 12 warps (16 for INT8/INT4):
 //   warps 0-3, 4-7  softmax of half 0 and half 1, a thread per query row
 //   warp 8          issues the matrix instructions (one lane)
-//   warp 9          bf16 pools: TMA copies of Q and of the paged K/V blocks
-//                   (a block is 16 rows: 2 KiB boxes in the 128-byte swizzle)
-//   warps 9-11      INT8/INT4 pools: read the codes, write them as bf16 (exact:
-//                   8 significant bits) into the same tiles; the K scale
-//                   multiplies the scores, the V scale the weights
+//   warp 9          TMA copies of Q and of the paged K/V blocks (bf16: a block is 16
+//                   rows, 2 KiB boxes in the 128-byte swizzle)
+//   warps 10-15     INT8/INT4 pools: write the codes that warp 9 copies as bf16
+//                   (exact: 8 significant bits) into the same tiles; the K
+//                   scale multiplies the scores, the V scale the weights
 // Tensor memory (512 columns): scores of both halves (128 fp32 columns each), their
 // outputs (d_h columns each). The weights P overwrite their half's
 // scores as bf16 and are the A operand of P V: one rounding of 2^-8 relative
@@ -41,12 +41,12 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
 constexpr int kRows = 128;       // query rows of a half, keys of a tile
 constexpr int kTileBlocks = kRows / kBlockTokens;
 constexpr int kPart = kRows / 2; // keys of one softmax step
 constexpr int kUnitRows = 2 * kRows;
-constexpr int kLoaders = 96;     // INT8/INT4 loader threads
+constexpr int kConvWarps = 6;    // INT8/INT4: warps that turn codes into bf16
 constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
 constexpr float kMoveLog2 = 8.f; // see above
 
@@ -218,12 +218,18 @@ struct MergeState {
 template <int D, int KIND>
 struct Smem {
     static constexpr int TILE = kRows * D * 2; // one Q half, K tile or V tile in bf16
-    static constexpr int SLOTS = D == 128 ? 4 : 8;
+    static constexpr int kThreads = KIND ? (kCopyWarp + 1 + kConvWarps) * 32 : 384;
+    // tiles in bf16, and (INT8/INT4) tiles of codes on their way
+    static constexpr int SLOTS = (KIND ? 3 : 4) * (128 / D);
+    static constexpr int ROWB = KIND == 1 ? D : D / 2;
+    static constexpr int RAW = kRows * ROWB + 2 * kRows * 4; // codes, K and V scales
+    static constexpr int RAWS = KIND == 0 ? 0 : KIND == 1 ? SLOTS : 6;
     static constexpr int kOffRing = 2 * TILE;
     static constexpr int kOffScales = kOffRing + SLOTS * TILE; // [ring][K, V][128] fp32
     static constexpr int kScaleBytes = KIND ? kScaleRing * 2 * kRows * 4 : 0;
-    static constexpr int kOffBars = kOffScales + kScaleBytes;
-    static constexpr int kBars = 2 + 2 * SLOTS + 10 + 1;
+    static constexpr int kOffRaw = kOffScales + kScaleBytes;
+    static constexpr int kOffBars = kOffRaw + RAWS * RAW;
+    static constexpr int kBars = 2 + 2 * SLOTS + 10 + 1 + 2 * RAWS;
     static constexpr int kOffMisc = kOffBars + (kBars * 8 + 15) / 16 * 16; // 64 int32
     static constexpr int kBytes = 1024 + kOffMisc + 256;
 };
@@ -235,15 +241,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tma
                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_stream_128(const uint4 *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
@@ -325,12 +322,12 @@ __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity)
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Smem<D, KIND>::kThreads, 1)
 cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const CrossParams p)
 {
     using L = Smem<D, KIND>;
-    constexpr int SLOTS = L::SLOTS, TILE = L::TILE, HALVES = D / 64;
+    constexpr int kThreads = L::kThreads, SLOTS = L::SLOTS, TILE = L::TILE, HALVES = D / 64;
     constexpr int COL = TILE / HALVES; // bytes of one 64-element column of a tile
     constexpr int RECORD = record_floats(D);
     extern __shared__ uint8_t smem_raw[];
@@ -342,12 +339,15 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     const uint32_t q_full = bars, q_empty = bars + 8, kv_full = bars + 16,
                    kv_empty = kv_full + 8 * SLOTS, s_full = kv_empty + 8 * SLOTS,
                    p_full = s_full + 16 /* [half][part] */, o_full = p_full + 32,
-                   a_full = o_full + 16, drained = a_full + 16;
+                   a_full = o_full + 16, drained = a_full + 16, raw_full = drained + 8,
+                   raw_empty = raw_full + 8 * L::RAWS;
     // misc: [0] tensor memory base (0), [1] merge flag, [2..3] start sequence and
-    // position, [8..] bad-block masks per slot, [16..17] per half, [24..] scan
+    // position, [8..] bad-block masks per slot, [16..17] per half, [18..23] blocks of
+    // the tiles of codes, [24..] scan
     int32_t *misc = reinterpret_cast<int32_t *>(smem + L::kOffMisc);
     volatile int32_t *slot_mask = misc + 8;
     volatile int32_t *half_mask = misc + 16;
+    volatile int32_t *raw_mask = misc + 18; // present blocks | bad ones << 8
 
     auto record = [&](int64_t i) { return p.records + i * RECORD; };
 
@@ -416,7 +416,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(kv_full + 8 * s, KIND ? kLoaders : 1);
+            mbar_init(kv_full + 8 * s, KIND ? kConvWarps : 1);
             mbar_init(kv_empty + 8 * s, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -427,9 +427,13 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             mbar_init(a_full + 8 * i, 1);
         }
         mbar_init(drained, 1);
+        for (int s = 0; s < L::RAWS; ++s) {
+            mbar_init(raw_full + 8 * s, 1);
+            mbar_init(raw_empty + 8 * s, kConvWarps);
+        }
         fence_barrier_init();
     }
-    if (warp == 8)
+    if (warp == kMmaWarp)
         tmem_alloc(smem_u32(misc), 512); // all of it: its base address is 0
     tc_fence_before();
     __syncthreads();
@@ -447,9 +451,10 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         return !dead;
     };
 
-    if (warp < 8) {
+    if (warp < kMmaWarp) {
         // ================================================================ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (KIND != 0) // 256 x 160 + 256 x 96 = the 512 x 128 of the launch
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int half = warp >> 2;
         const int r = half * kRows + (tid & (kRows - 1)); // row within the unit
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // lane base of this warp, bits 16..
@@ -472,8 +477,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 tmem_ld32(tS + 32, s + 32);
                 tmem_wait_ld();
                 tmem_landed<kPart>(s);
-                tmem_ld32(tS + 64, s + 64);
-                tmem_ld32(tS + 96, s + 96);
                 const float *sk =
                     scales + ((n_tile + (uint32_t)(j - g.j0)) % kScaleRing) * 2 * kRows;
                 const int tail = ctx % kBlockTokens;
@@ -496,6 +499,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 for (int part = 0; part < 2; ++part) {
                     const int c0 = part * kPart;
                     if (part == 1) {
+                        tmem_ld32(tS + 64, s + 64);
+                        tmem_ld32(tS + 96, s + 96);
                         tmem_wait_ld();
                         tmem_landed<kPart>(s + kPart);
                     }
@@ -682,8 +687,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8) {
+        if constexpr (KIND != 0)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == kMmaWarp) {
             // ======================================================== matrix instructions
             // One thread runs the whole loop: a warp would pay a vote and a broadcast at each
             // of its waits and operands, which come one after another. The halves take strict
@@ -799,28 +805,16 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
             }
             __syncwarp();
-        } else if (KIND != 0 || warp == 9) {
+        } else if (warp == kCopyWarp) {
             // ============================================================== copies
-            uint32_t n_q = 0, n_kv = 0, n_tile = 0;
-            auto load_q = [&]() { // (warp 9 alone: the barrier does not wait for the others)
-                if (warp != 9 || !wait(q_empty, n_q + 1))
-                    return;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, (uint32_t)(g.halves * TILE));
-                    const int32_t t0 = (int32_t)(walk.s.q0 + g.row0 / p.g);
-                    for (int i = 0; i < g.halves; ++i)
-                        for (int c = 0; c < HALVES; ++c)
-                            tma_load_3d(sbase + i * TILE + c * COL, &tmQ, c * 64, g.kvh * p.g,
-                                        t0 + i * (kRows / p.g), q_full);
-                }
-                __syncwarp();
-                ++n_q;
-            };
+            uint32_t n_q = 0, n_kv = 0;
+            // ring of the copies: bf16 tiles, or tiles of codes
+            constexpr int RING = KIND ? L::RAWS : SLOTS;
+            const uint32_t full0 = KIND ? raw_full : kv_full, empty0 = KIND ? raw_empty : kv_empty;
             while (walk.next(g) && !dead) {
-                const int ctx = walk.s.ctx;
-                const int nblk = (int)(((int64_t)ctx + kBlockTokens - 1) / kBlockTokens);
+                const int nblk = (int)(((int64_t)walk.s.ctx + kBlockTokens - 1) / kBlockTokens);
                 const int32_t *table = p.block_tables + (int64_t)walk.b * p.max_blocks;
-                for (int j = g.j0; j < g.j1; ++j, ++n_tile) {
+                for (int j = g.j0; j < g.j1; ++j) {
                     // lanes 0-7 (and their copies): the tile's eight blocks
                     const int blk = j * kTileBlocks + (lane & 7);
                     const int32_t phys = blk < nblk ? __ldg(table + blk) : -1;
@@ -829,128 +823,168 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         __ballot_sync(0xffffffffu, blk < nblk && !ok) & 0xffu;
                     if (bad && lane == 0)
                         flag_error(p.dev_status, PA_DEV_BAD_BLOCK_BIT);
+                    const uint32_t have = __ballot_sync(0xffffffffu, ok) & 0xffu;
                     const int32_t prow = ok ? phys * p.n_kv + g.kvh : -1; // (block, head) tile
+                    int32_t rows[kTileBlocks];
+#pragma unroll
+                    for (int i = 0; i < kTileBlocks; ++i)
+                        rows[i] = __shfl_sync(0xffffffffu, prow, i);
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv, ++n_kv) {
-                        const uint32_t slot = n_kv % SLOTS;
-                        if (!wait(kv_empty + 8 * slot, n_kv / SLOTS + 1))
+                        const uint32_t slot = n_kv % RING;
+                        if (!wait(empty0 + 8 * slot, n_kv / RING + 1))
                             break;
-                        const uint32_t full = kv_full + 8 * slot, dst = ring + slot * TILE;
-                        if (warp == 9 && lane == 0)
-                            slot_mask[slot] = (int32_t)bad;
-                        __syncwarp();
+                        const uint32_t full = warp_uniform(full0 + 8 * slot);
                         if constexpr (KIND == 0) {
-                            // absent and bad blocks: a box outside the pool arrives as zeros
-                            const int32_t y =
-                                ok ? prow * kBlockTokens
-                                   : (int32_t)(p.num_blocks * p.n_kv * kBlockTokens);
-                            int32_t ys[kTileBlocks];
-#pragma unroll
-                            for (int i = 0; i < kTileBlocks; ++i)
-                                ys[i] = __shfl_sync(0xffffffffu, y, i);
                             const CUtensorMap *tm = kv ? &tmV : &tmK;
-                            const uint32_t d0 = warp_uniform(dst), f0 = warp_uniform(full);
+                            const uint32_t dst = warp_uniform(ring + slot * TILE);
                             if (elect_one()) {
                                 const uint64_t pol = l2_policy_evict_normal();
-                                mbar_arrive_expect_tx(f0, TILE);
+                                slot_mask[slot] = (int32_t)bad;
+                                mbar_arrive_expect_tx(full, TILE);
+                                // absent and bad blocks: a box outside the pool arrives as zeros
+                                const int32_t outside =
+                                    (int32_t)(p.num_blocks * p.n_kv * kBlockTokens);
 #pragma unroll
-                                for (int i = 0; i < kTileBlocks; ++i)
+                                for (int i = 0; i < kTileBlocks; ++i) {
+                                    const int32_t y = rows[i] >= 0 ? rows[i] * kBlockTokens : outside;
 #pragma unroll
                                     for (int c = 0; c < HALVES; ++c)
-                                        tma_load_2d(d0 + c * COL + i * 2048, tm, c * 64, ys[i], f0, pol);
+                                        tma_load_2d(dst + c * COL + i * 2048, tm, c * 64, y, full,
+                                                    pol);
+                                }
                             }
-                            __syncwarp();
                         } else {
-                            constexpr int ROWB = KIND == 1 ? D : D / 2;
-                            constexpr int CPR = ROWB / 16; // 16-byte chunks per row
-                            constexpr int CHUNKS = kRows * CPR;
-                            constexpr int PER = (CHUNKS + kLoaders - 1) / kLoaders;
-                            constexpr int BATCH = 6;
-                            const int t = tid - 9 * 32;
+                            constexpr uint32_t BLOCK = kBlockTokens * L::ROWB;
                             const uint8_t *pool =
                                 static_cast<const uint8_t *>(kv ? p.v_cache : p.k_cache);
-                            if (kv == 0) { // the tile's scales, both kinds
-                                float *sc = reinterpret_cast<float *>(smem + L::kOffScales) +
-                                            (n_tile % kScaleRing) * 2 * kRows;
+                            const uint32_t dst = warp_uniform(sbase + L::kOffRaw + slot * L::RAW);
+                            if (elect_one()) {
+                                const uint64_t pol = l2_policy_evict_normal();
+                                raw_mask[slot] = (int32_t)(have | bad << 8);
+                                // the K tile brings the scales of both
+                                mbar_arrive_expect_tx(full, __popc(have) * (BLOCK + (kv ? 0 : 128)));
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int r = t + e * kLoaders;
-                                    const int32_t pr = __shfl_sync(0xffffffffu, prow, (r >> 4) & 7);
-                                    if (r < kRows) {
-                                        const bool in = pr >= 0 && j * kRows + r < ctx;
-                                        const int64_t at = (int64_t)pr * kBlockTokens + (r & 15);
-                                        sc[r] = in ? __ldg(p.k_scale + at) * p.scale_log2 : 0.f;
-                                        sc[kRows + r] = in ? __ldg(p.v_scale + at) : 0.f;
-                                    }
-                                }
-                            }
-#pragma unroll 1
-                            for (int e0 = 0; e0 < PER; e0 += BATCH) {
-                                uint4 x[BATCH];
-#pragma unroll
-                                for (int e = 0; e < BATCH; ++e) {
-                                    const int c = (e0 + e) * kLoaders + t, r = c / CPR;
-                                    const int32_t pr = __shfl_sync(0xffffffffu, prow, (r >> 4) & 7);
-                                    x[e] = make_uint4(0, 0, 0, 0);
-                                    if (c < CHUNKS && pr >= 0 && j * kRows + r < ctx)
-                                        x[e] = ld_stream_128(reinterpret_cast<const uint4 *>(pool) +
-                                                             (int64_t)pr * (kBlockTokens * CPR) +
-                                                             (r & 15) * CPR + c % CPR);
-                                }
-#pragma unroll
-                                for (int e = 0; e < BATCH; ++e) {
-                                    const int c = (e0 + e) * kLoaders + t, r = c / CPR;
-                                    if (c >= CHUNKS)
+                                for (int i = 0; i < kTileBlocks; ++i) {
+                                    if (rows[i] < 0)
                                         continue;
-                                    // first 16-byte chunk of 8 bf16 that this one becomes
-                                    const int o = c % CPR * (KIND == 1 ? 2 : 4);
-                                    auto put = [&](int i, uint32_t a, uint32_t b, uint32_t cc,
-                                                   uint32_t d) {
-                                        const int oc = o + i;
-                                        sts128(dst + (oc / 8) * COL + r * 128 +
-                                                   (((oc % 8) ^ (r & 7)) << 4),
-                                               a, b, cc, d);
-                                    };
-                                    const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-                                    if constexpr (KIND == 1) {
-#pragma unroll
-                                        for (int i = 0; i < 2; ++i)
-                                            put(i, code8_bf2<0x4140>(w[2 * i]),
-                                                code8_bf2<0x4342>(w[2 * i]),
-                                                code8_bf2<0x4140>(w[2 * i + 1]),
-                                                code8_bf2<0x4342>(w[2 * i + 1]));
-                                    } else {
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
-                                            put(i, code4_bf2<0>(a, b), code4_bf2<1>(a, b),
-                                                code4_bf2<2>(a, b), code4_bf2<3>(a, b));
-                                        }
+                                    bulk_load_1d(dst + i * BLOCK, pool + (int64_t)rows[i] * BLOCK,
+                                                 BLOCK, full, pol);
+                                    if (kv == 0) {
+                                        const int64_t at = (int64_t)rows[i] * kBlockTokens;
+                                        const uint32_t sc = dst + kRows * L::ROWB + i * 64;
+                                        bulk_load_1d(sc, p.k_scale + at, 64, full, pol);
+                                        bulk_load_1d(sc + kRows * 4, p.v_scale + at, 64, full, pol);
                                     }
                                 }
                             }
-                            fence_proxy_async_smem();
-                            mbar_arrive(full);
                         }
+                        __syncwarp();
                     }
                     if (dead)
                         break;
-                    if (j == g.j0)
-                        load_q();
+                    if (j == g.j0) { // the unit's queries, once the last unit's are read
+                        if (!wait(q_empty, n_q + 1))
+                            break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(q_full, (uint32_t)(g.halves * TILE));
+                            const int32_t t0 = (int32_t)(walk.s.q0 + g.row0 / p.g);
+                            for (int i = 0; i < g.halves; ++i)
+                                for (int c = 0; c < HALVES; ++c)
+                                    tma_load_3d(sbase + i * TILE + c * COL, &tmQ, c * 64,
+                                                g.kvh * p.g, t0 + i * (kRows / p.g), q_full);
+                        }
+                        __syncwarp();
+                        ++n_q;
+                    }
                 }
             }
-            if (KIND == 0 && dead) { // copies in flight land (bounded) before the memory goes
-                for (uint32_t n = n_kv > SLOTS ? n_kv - SLOTS : 0; n < n_kv; ++n)
-                    mbar_wait(kv_full + 8 * (n % SLOTS), (n / SLOTS) & 1u);
+            if (dead) { // copies in flight land (bounded) before the memory goes
+                for (uint32_t n = n_kv > RING ? n_kv - RING : 0; n < n_kv; ++n)
+                    mbar_wait(full0 + 8 * (n % RING), (n / RING) & 1u);
+                if (n_q)
+                    mbar_wait(q_full, (n_q - 1) & 1u);
             }
-            if (dead && n_q)
-                mbar_wait(q_full, (n_q - 1) & 1u);
+        } else if constexpr (KIND != 0) {
+            // ======================================================= codes into bf16
+            constexpr int CPR = L::ROWB / 16; // 16-byte chunks per row
+            constexpr int CHUNKS = kRows * CPR, CONV = kConvWarps * 32;
+            const int t = tid - (kCopyWarp + 1) * 32;
+            uint32_t n_kv = 0, n_tile = 0;
+            while (walk.next(g) && !dead) {
+                for (int j = g.j0; j < g.j1 && !dead; ++j, ++n_tile) {
+                    const int valid = min(walk.s.ctx - j * kRows, kRows);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++n_kv) {
+                        const uint32_t from = n_kv % L::RAWS, slot = n_kv % SLOTS;
+                        if (!wait(raw_full + 8 * from, n_kv / L::RAWS) ||
+                            !wait(kv_empty + 8 * slot, n_kv / SLOTS + 1))
+                            break;
+                        const uint32_t dst = ring + slot * TILE;
+                        const uint8_t *raw = smem + L::kOffRaw + from * L::RAW;
+                        const int mask = raw_mask[from];
+                        // rows of absent and bad blocks and behind the context are zero
+                        auto present = [&](int r) {
+                            return r < valid && ((mask >> (r / kBlockTokens)) & 1);
+                        };
+                        if (t == 0)
+                            slot_mask[slot] = mask >> 8;
+                        if (kv == 0 && t < kRows) {
+                            const float *in = reinterpret_cast<const float *>(raw + kRows * L::ROWB);
+                            float *sc = reinterpret_cast<float *>(smem + L::kOffScales) +
+                                        (n_tile % kScaleRing) * 2 * kRows;
+                            sc[t] = present(t) ? in[t] * p.scale_log2 : 0.f;
+                            sc[kRows + t] = present(t) ? in[kRows + t] : 0.f;
+                        }
+#pragma unroll 3
+                        for (int c = t; c < CHUNKS; c += CONV) {
+                            const int r = c / CPR, cr = c % CPR;
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if (present(r))
+                                x = *reinterpret_cast<const uint4 *>(raw + 16 * c);
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            // 16-byte chunk oc of the row's bf16 values
+                            auto put = [&](int oc, uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
+                                sts128(dst + (oc / 8) * COL + r * 128 + (((oc % 8) ^ (r & 7)) << 4),
+                                       a, b, d, e);
+                            };
+                            if constexpr (KIND == 1) {
+                                // (a row's second 64 columns take its chunks in the other order: the
+                                // eight threads of a row then write to different banks)
+                                const int flip = CPR == 8 ? cr >> 2 : 0;
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const bool up = i ^ flip;
+                                    const uint32_t a = up ? w[2] : w[0], b = up ? w[3] : w[1];
+                                    put(2 * cr + up, code8_bf2<0x4140>(a), code8_bf2<0x4342>(a),
+                                        code8_bf2<0x4140>(b), code8_bf2<0x4342>(b));
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
+                                    // (a row without codes is zero, not minus eight)
+                                    const uint32_t z = present(r) ? 0xffffffffu : 0u;
+                                    put(4 * cr + i, code4_bf2<0>(a, b) & z, code4_bf2<1>(a, b) & z,
+                                        code4_bf2<2>(a, b) & z, code4_bf2<3>(a, b) & z);
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(kv_full + 8 * slot);
+                            mbar_arrive(raw_empty + 8 * from);
+                        }
+                    }
+                }
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8)
+    if (warp == kMmaWarp)
         tmem_dealloc(tmem, 512);
 }
 
@@ -964,7 +998,7 @@ cudaError_t launch_of(const CUtensorMap &tq, const CUtensorMap &tk, const CUtens
         cross_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess)
         return e;
-    cross_kernel<D, KIND><<<p.num_ctas, kThreads, bytes, stream>>>(tq, tk, tv, p);
+    cross_kernel<D, KIND><<<p.num_ctas, Smem<D, KIND>::kThreads, bytes, stream>>>(tq, tk, tv, p);
     return cudaGetLastError();
 }
 

@@ -39,6 +39,7 @@ def test_argument_checks(lib):
     for kw in (dict(q=ODD), dict(cu=ODD), dict(kc=ODD), dict(out=ODD), dict(bt=ODD),
                dict(ctx=ODD), dict(ws=ctypes.c_void_p(272))):
         assert call(**kw) == -11, kw
+    assert call(g=_geom(kv_dtype=1), ks=ctypes.c_void_p(264)) == -11
     assert call(ks=FAKE) == -2 and call(g=_geom(kv_dtype=1)) == -1
     assert call(g=_geom(d_h=96)) == -4 and call(g=_geom(n_h=30)) == -2
     assert call(g=_geom(kv_dtype=9)) == -3
