@@ -11,9 +11,9 @@
 // Split. The query rows of a kv head (tokens x the g heads that share it) are
 // packed: row t * g + h. A unit is (sequence, kv head, up to 256 packed rows),
 // one or two halves of 128 rows = one tensor-core tile each; its items are
-// the 128-key tiles of the context. Items lie on one line, an item as long as
-// its halves, and CTA c of G takes [c W / G, (c + 1) W / G) of it, so any mix of
-// lengths is balanced and a few long contexts still use every SM. A unit cut
+// the 128-key tiles of the context. Items lie on one line (one or two halves
+// take about as long) and CTA c of G takes [c W / G, (c + 1) W / G) of it, so any
+// mix of lengths is balanced and a few long contexts still use every SM. A unit cut
 // by CTA borders leaves (m, l, O) records; the last CTA to finish it merges them
 // (log-sum-exp). No CTA waits for another.
 //
@@ -29,7 +29,9 @@
 // outputs (d_h columns each). The weights P overwrite their half's
 // scores as bf16 and are the A operand of P V: one rounding of 2^-8 relative
 // per weight, of the size of the output's own; sums l take the unrounded
-// weights. While one half is in its softmax the other has the tensor cores.
+// weights. While one half is in its softmax the other has the tensor cores. A
+// unit of one half uses both sets in turn, tile after tile, and joins its two
+// states at the end.
 //
 // The softmax base of a row moves only when a tile's maximum exceeds it by more
 // than 2^8 (exact: P, l and O share one base), so O is rarely rescaled.
@@ -75,8 +77,8 @@ struct CrossParams {
 struct Seq {
     int32_t ctx, q0, nq;
     int32_t tiles;  // 128-key tiles
-    int32_t halves; // 128-row halves of one kv head's query rows
-    __device__ int64_t cost(int n_kv) const { return (int64_t)n_kv * tiles * halves; }
+    int32_t units;  // units of up to 256 packed query rows, of one kv head
+    __device__ int64_t items(int n_kv) const { return (int64_t)n_kv * tiles * units; }
 };
 
 // Sequence b's sizes; bad ones (reported where `report`) count as nothing.
@@ -93,7 +95,7 @@ __device__ __forceinline__ Seq load_seq(const CrossParams &p, int b, bool report
     s.q0 = q_ok ? q0 : 0;
     s.nq = q_ok ? q1 - q0 : 0;
     s.tiles = (int32_t)(((int64_t)s.ctx + kRows - 1) / kRows);
-    s.halves = (int32_t)(((int64_t)s.nq * p.g + kRows - 1) / kRows);
+    s.units = (int32_t)(((int64_t)s.nq * p.g + kUnitRows - 1) / kUnitRows);
     return s;
 }
 
@@ -125,32 +127,27 @@ struct Walk {
 
     __device__ bool next(Segment &g)
     {
-        while (pos < hi) {
-            int64_t c = s.cost(p.n_kv);
+        if (pos < hi) {
+            int64_t c = s.items(p.n_kv);
             while (pos >= vb + c) { // (pos is below the line's end, so b stays in range)
                 vb += c;
                 s = load_seq(p, ++b, false);
-                c = s.cost(p.n_kv);
+                c = s.items(p.n_kv);
             }
-            const int64_t head = (int64_t)s.tiles * s.halves;
+            const int64_t head = (int64_t)s.tiles * s.units;
             int64_t r = pos - vb;
             g.kvh = (int)div_small(r, head);
             r -= g.kvh * head;
-            const int64_t pair = 2 * (int64_t)s.tiles;
-            const int64_t qt = div_small(r, pair);
-            const int64_t off = r - qt * pair;
-            g.halves = (int)min((int64_t)2, s.halves - 2 * qt);
-            g.first_v = pos - off;
-            const int64_t end = g.first_v + (int64_t)s.tiles * g.halves;
-            // an item belongs to the CTA that has its first position
-            g.j0 = (int)((off + g.halves - 1) / g.halves);
-            g.j1 = hi >= end ? s.tiles : (int)((hi - g.first_v + g.halves - 1) / g.halves);
+            const int64_t qt = div_small(r, s.tiles);
+            g.j0 = (int)(r - qt * s.tiles);
+            g.first_v = pos - g.j0;
+            const int64_t end = g.first_v + s.tiles;
+            g.j1 = hi >= end ? s.tiles : (int)(hi - g.first_v);
             g.leading = pos == lo;
             pos = end;
-            if (g.j0 >= g.j1)
-                continue;
             g.row0 = qt * kUnitRows;
             g.rows = (int)min((int64_t)kUnitRows, (int64_t)s.nq * p.g - g.row0);
+            g.halves = g.rows > kRows ? 2 : 1;
             g.whole = g.j0 == 0 && g.j1 == s.tiles;
             return true;
         }
@@ -231,7 +228,8 @@ struct Smem {
     static constexpr int kOffBars = kOffRaw + RAWS * RAW;
     static constexpr int kBars = 2 + 2 * SLOTS + 10 + 1 + 2 * RAWS;
     static constexpr int kOffMisc = kOffBars + (kBars * 8 + 15) / 16 * 16; // 64 int32
-    static constexpr int kBytes = 1024 + kOffMisc + 256;
+    static constexpr int kOffRows = kOffMisc + 256; // (m, l) [buffer][128]
+    static constexpr int kBytes = 1024 + kOffRows + 2 * kRows * 8;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tmap, int32_t x,
@@ -256,6 +254,11 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
     uint32_t r;
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+__device__ __forceinline__ void bar_named(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Two fp32 lanes per instruction.
@@ -361,7 +364,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         const int b0 = min(tid * per, p.num_seqs), b1 = min(b0 + per, p.num_seqs);
         int64_t sum = 0;
         for (int b = b0; b < b1; ++b)
-            sum += load_seq(p, b, blockIdx.x == 0).cost(p.n_kv);
+            sum += load_seq(p, b, blockIdx.x == 0).items(p.n_kv);
         int64_t x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -380,14 +383,13 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             total += wsum[w];
         }
         if (total > 0) {
-            // at least two positions per CTA: each then owns an item
-            const int64_t G = max((int64_t)1, plan_ctas(p.num_ctas, total / 2));
+            const int64_t G = plan_ctas(p.num_ctas, total);
             const int64_t lo = plan_lo(blockIdx.x, total, G);
             if (blockIdx.x < G && lo >= before && lo < before + sum) {
                 int b = b0;
                 int64_t v = before;
                 for (;; ++b) { // the sequence that holds position lo (there is one)
-                    const int64_t c = load_seq(p, b, false).cost(p.n_kv);
+                    const int64_t c = load_seq(p, b, false).items(p.n_kv);
                     if (lo < v + c)
                         break;
                     v += c;
@@ -407,8 +409,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    const int64_t G = max((int64_t)1, plan_ctas(p.num_ctas, total / 2));
-    if (total == 0 || blockIdx.x >= G)
+    const int64_t G = plan_ctas(p.num_ctas, total);
+    if (blockIdx.x >= G) // (no items: no CTA)
         return;
     const int64_t lo = plan_lo(blockIdx.x, total, G), hi = plan_lo(blockIdx.x + 1, total, G);
 
@@ -456,17 +458,23 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         if constexpr (KIND != 0) // 256 x 160 + 256 x 96 = the 512 x 128 of the launch
             asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int half = warp >> 2;
-        const int r = half * kRows + (tid & (kRows - 1)); // row within the unit
+        const int row = tid & (kRows - 1);
+        // (m, l) of each buffer's rows, where the two buffers share a half's rows
+        float2 *states = reinterpret_cast<float2 *>(smem + L::kOffRows);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // lane base of this warp, bits 16..
         const uint32_t tS = tmem + lanes + half * 128, tO = tmem + lanes + 256 + half * 128;
         const float *scales = reinterpret_cast<const float *>(smem + L::kOffScales);
-        uint32_t n_s = 0;     // tiles of this half so far
+        uint32_t n_b[2] = {0, 0}; // tiles of each buffer so far
         uint32_t n_tile = 0;  // tiles of this CTA so far (the scale ring's index)
         while (walk.next(g)) {
             const int ctx = walk.s.ctx;
             float m = -INFINITY, l = 0.f;
-            const bool mine = half < g.halves;
-            for (int j = g.j0; mine && j < g.j1; ++j, ++n_s) {
+            // two halves: each buffer one half, every tile; one half: both buffers its rows,
+            // every other tile
+            const bool two = g.halves == 2;
+            const int j_first = two ? g.j0 : g.j0 + half, step = two ? 1 : 2;
+            uint32_t n_s = half ? n_b[1] : n_b[0];
+            for (int j = j_first; j < g.j1; j += step, ++n_s) {
                 if (!wait(s_full + 8 * half, n_s))
                     break;
                 tc_fence_after();
@@ -538,7 +546,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     const float top = mul * fmaxf(max3(mx[0], end[0], end[1]),
                                                   fmaxf(max3(mx[1], end[2], end[3]),
                                                         fmaxf(mx[2], mx[3])));
-                    if (part == 0 && j == g.j0) {
+                    if (part == 0 && j == j_first) {
                         m = top;
                     } else {
                         const bool up = top > m + kMoveLog2;
@@ -595,17 +603,39 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     mbar_arrive(p_full + 16 * half + 8 * part);
                 }
             }
-            n_tile += (uint32_t)(g.j1 - g.j0);
+            const int n = g.j1 - g.j0;
+            n_tile += (uint32_t)n;
+            n_b[0] += two ? n : (n + 1) / 2;
+            n_b[1] += two ? n : n / 2;
             // ---- the half's output, or its record
-            const bool live = mine && r < g.rows;
-            const int64_t row = g.row0 + r; // packed row of (sequence, kv head)
-            if (mine) {
+            const int r = two ? half * kRows + row : row; // row within the unit
+            const bool live = r < g.rows;
+            const int64_t prow = g.row0 + r; // packed row of (sequence, kv head)
+            const int64_t t = prow / p.g, h = prow - t * p.g;
+            __nv_bfloat16 *o_row = p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D;
+            float *rec = record((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1));
+            // 32 outputs from column c on, of a row whose weights sum to l
+            auto emit = [&](int c, const float (&o)[32], float inv) {
+                if (live && g.whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(o_row + c + e) =
+                            make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv),
+                                       pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                       pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                                       pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        reinterpret_cast<float4 *>(rec)[(c + e) / 4 * kUnitRows + r] =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            };
+            // (a sum that is not a number must not be skipped for its base)
+            m = l != l ? 0.f : m;
+            if (two) {
                 wait(o_full + 8 * half, n_s - 1);
                 tc_fence_after();
-                const int64_t t = row / p.g, h = row - t * p.g;
-                __nv_bfloat16 *o_row =
-                    p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D;
-                float *rec = record((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1));
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll 1
                 for (int c = 0; !dead && c < D; c += 32) {
@@ -613,32 +643,54 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     tmem_ld32(tO + c, o);
                     tmem_wait_ld();
                     tmem_landed<32>(o);
-                    if (live && g.whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(o_row + c + e) = make_uint4(
-                                pack_bf16x2(o[e] * inv, o[e + 1] * inv),
-                                pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
-                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
-                                pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
-                    } else if (live) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            reinterpret_cast<float4 *>(rec)[(c + e) / 4 * kUnitRows + r] =
-                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    }
+                    emit(c, o, inv);
                 }
-                if (live && !g.whole) // (a sum that is not a number must not be skipped for its base)
-                    reinterpret_cast<float2 *>(rec + D * kUnitRows)[r] =
-                        make_float2(l != l ? 0.f : m, l);
-                tc_fence_before(); // (the next p_full orders these reads before the next products)
+            } else {
+                // both buffers' states of this row join; each thread takes half the columns
+                states[half * kRows + row] = make_float2(m, l);
+                bar_named(1, 2 * kRows);
+                const float2 s0 = states[row], s1 = states[kRows + row];
+                wait(o_full, n_b[0] - 1);
+                if (n > 1)
+                    wait(o_full + 8, n_b[1] - 1);
+                tc_fence_after();
+                m = fmaxf(s0.x, s1.x);
+                const float f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
+                const float f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - m);
+                l = fmaf(f0, s0.y, f1 * s1.y);
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll 1
+                for (int c = half * (D / 2); !dead && c < (half + 1) * (D / 2); c += 32) {
+                    float o[32];
+                    tmem_ld32(lanes + 256 + c, o);
+                    tmem_wait_ld();
+                    tmem_landed<32>(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] *= f0;
+                    if (n > 1) { // (else the second buffer holds nothing)
+                        float o1[32];
+                        tmem_ld32(lanes + 384 + c, o1);
+                        tmem_wait_ld();
+                        tmem_landed<32>(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = fmaf(f1, o1[e], o[e]);
+                    }
+                    emit(c, o, inv);
+                }
             }
+            if (live && !g.whole && (two || half == 0))
+                reinterpret_cast<float2 *>(rec + D * kUnitRows)[r] = make_float2(m, l);
+            tc_fence_before(); // (the next p_full orders these reads before the next products)
+            if (!two)
+                bar_named(1, 2 * kRows); // each buffer's outputs were read by both
             if (g.whole)
                 continue;
             // ---- a cut unit: the last CTA to arrive merges its records
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            bar_named(1, 2 * kRows);
             const int64_t c_first = plan_owner(g.first_v, total, G);
-            const int64_t last_v = g.first_v + (int64_t)(walk.s.tiles - 1) * g.halves;
+            const int64_t last_v = g.first_v + walk.s.tiles - 1;
             const int nseg = (int)(plan_owner(last_v, total, G) - c_first + 1);
             if (tid == 0) {
                 const int last = atomic_add_acq_rel_gpu(p.counters + c_first, 1) == nseg - 1;
@@ -646,7 +698,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     p.counters[c_first] = 0; // every arrival is in: ready for the next call
                 misc[1] = last;
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            bar_named(1, 2 * kRows);
             if (!misc[1])
                 continue;
             const int slot = g.first_v == plan_lo(c_first, total, G) ? 0 : 1;
@@ -716,7 +768,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 };
                 // scores of half I against the K tile in slot ks: Q K^T. The half's previous
                 // P V must be done: it reads P where the scores go.
-                auto scores = [&](auto half, uint32_t np, uint32_t ks, bool release, bool last) {
+                auto scores = [&](auto half, int q, uint32_t np, uint32_t ks, bool release, bool last) {
                     constexpr int I = decltype(half)::value;
                     const uint64_t k_desc = kHigh | (k_ring + ks * kSlotDesc);
                     half_mask[I] = slot_mask[ks]; // (the softmax is done with the last one)
@@ -727,7 +779,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk / 4) * COL + (kk % 4) * 32) >> 4;
-                        tc_mma_ss(I * 128, kHigh | (q_desc + I * kSlotDesc + off), k_desc + off, iS,
+                        tc_mma_ss(I * 128, kHigh | (q_desc + q * kSlotDesc + off), k_desc + off, iS,
                                   kk > 0);
                     }
                     tc_commit(s_full + 8 * I);
@@ -776,24 +828,49 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     uint32_t ks, vs;
                     if (!ready(q_full, n_q) || !take(ks))
                         break;
-                    scores(H0(), np0, ks, !two, !two && n == 1);
+                    scores(H0(), 0, np0, ks, !two, !two && n == 1);
                     if (!take(vs))
                         break;
+                    if (two) {
 #pragma unroll 1
-                    for (int jj = 0; jj < n && !dead; ++jj) {
-                        const bool more = jj + 1 < n;
-                        if (two)
-                            scores(H1(), np1, ks, true, !more);
-                        outputs(H0(), np0, vs, jj > 0, !two);
-                        if (more) {
+                        for (int jj = 0; jj < n && !dead; ++jj) {
+                            const bool more = jj + 1 < n;
+                            scores(H1(), 1, np1, ks, true, !more);
+                            outputs(H0(), np0, vs, jj > 0, false);
+                            if (more) {
+                                if (!take(ks))
+                                    break;
+                                scores(H0(), 0, np0, ks, false, false);
+                            }
+                            outputs(H1(), np1, vs, jj > 0, true);
+                            if (more && !take(vs))
+                                break;
+                        }
+                    } else { // one half: tiles alternate between the two buffers
+                        if (n > 1) {
                             if (!take(ks))
                                 break;
-                            scores(H0(), np0, ks, !two, !two && jj + 2 == n);
+                            scores(H1(), 0, np1, ks, true, n == 2);
                         }
-                        if (two)
+#pragma unroll 1
+                        for (int jj = 0; jj < n && !dead; jj += 2) {
+                            outputs(H0(), np0, vs, jj > 0, true);
+                            if (jj + 1 == n || !take(vs))
+                                break;
+                            if (jj + 2 < n) {
+                                if (!take(ks))
+                                    break;
+                                scores(H0(), 0, np0, ks, true, jj + 3 == n);
+                            }
                             outputs(H1(), np1, vs, jj > 0, true);
-                        if (more && !take(vs))
-                            break;
+                            if (jj + 2 < n && !take(vs))
+                                break;
+                            if (jj + 3 < n) {
+                                if (!take(ks))
+                                    break;
+                                scores(H1(), 0, np1, ks, true, jj + 4 == n);
+                            }
+                        }
                     }
                     if (dead)
                         break;
@@ -936,7 +1013,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                             sc[t] = present(t) ? in[t] * p.scale_log2 : 0.f;
                             sc[kRows + t] = present(t) ? in[kRows + t] : 0.f;
                         }
-#pragma unroll 3
+#pragma unroll 1 // (unrolled, its instructions push the other warps' out of the cache)
                         for (int c = t; c < CHUNKS; c += CONV) {
                             const int r = c / CPR, cr = c % CPR;
                             uint4 x = make_uint4(0, 0, 0, 0);
