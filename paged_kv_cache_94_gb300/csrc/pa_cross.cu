@@ -38,8 +38,6 @@
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
 
-#include <type_traits>
-
 namespace pa {
 namespace {
 
@@ -480,11 +478,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 tc_fence_after();
                 const int bad = half_mask[half];
                 const int valid = min(ctx - j * kRows, kRows);
-                float s[kRows];
-                tmem_ld32(tS, s);
-                tmem_ld32(tS + 32, s + 32);
-                tmem_wait_ld();
-                tmem_landed<kPart>(s);
                 const float *sk =
                     scales + ((n_tile + (uint32_t)(j - g.j0)) % kScaleRing) * 2 * kRows;
                 const int tail = ctx % kBlockTokens;
@@ -503,21 +496,22 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
                 // The tile's two halves of 64 keys are two steps of the online softmax: the
                 // products of the first start while the weights of the second are formed.
-#pragma unroll
+                // (One copy of the code for both: unrolled, the kernel's loops no longer fit the
+                // instruction cache together.)
+#pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     const int c0 = part * kPart;
-                    if (part == 1) {
-                        tmem_ld32(tS + 64, s + 64);
-                        tmem_ld32(tS + 96, s + 96);
-                        tmem_wait_ld();
-                        tmem_landed<kPart>(s + kPart);
-                    }
+                    float s[kPart];
+                    tmem_ld32(tS + c0, s);
+                    tmem_ld32(tS + c0 + 32, s + 32);
+                    tmem_wait_ld();
+                    tmem_landed<kPart>(s);
                     // scores in the log2 domain = s * mul
                     float mul = p.scale_log2;
                     if constexpr (KIND != 0) {
 #pragma unroll
-                        for (int c = c0; c < c0 + kPart; c += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sk + c);
+                        for (int c = 0; c < kPart; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sk + c0 + c);
                             const float2 a =
                                 mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
                             const float2 b =
@@ -530,19 +524,20 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         mul = 1.f;
                     }
                     if (valid < kRows || bad || mul < 0.f) {
+                        const int here = valid - c0, bad_here = bad >> (c0 / kBlockTokens);
 #pragma unroll
-                        for (int c = c0; c < c0 + kPart; ++c)
-                            s[c] = c < valid && !((bad >> (c / kBlockTokens)) & 1) ? s[c] * mul
-                                                                                   : -INFINITY;
+                        for (int c = 0; c < kPart; ++c)
+                            s[c] = c < here && !((bad_here >> (c / kBlockTokens)) & 1) ? s[c] * mul
+                                                                                       : -INFINITY;
                         mul = 1.f;
                     }
-                    float mx[4] = {s[c0], s[c0 + 1], s[c0 + 2], s[c0 + 3]};
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int c = c0 + 4; c < c0 + kPart - 4; c += 8)
+                    for (int c = 4; c < kPart - 4; c += 8)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-                    const float *end = s + c0 + kPart - 4;
+                    const float *end = s + kPart - 4;
                     const float top = mul * fmaxf(max3(mx[0], end[0], end[1]),
                                                   fmaxf(max3(mx[1], end[2], end[3]),
                                                         fmaxf(mx[2], mx[3])));
@@ -582,7 +577,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         float2 x[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int at = c0 + e + 2 * i;
+                            const int at = e + 2 * i;
                             x[i] = fma2(make_float2(s[at], s[at + 1]), mul_2, base_2);
                             x[i].x = fast_exp2(x[i].x);
                             x[i].y = fast_exp2(x[i].y);
@@ -744,9 +739,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         if (warp == kMmaWarp) {
             // ======================================================== matrix instructions
             // One thread runs the whole loop: a warp would pay a vote and a broadcast at each
-            // of its waits and operands, which come one after another. The halves take strict
-            // turns (P V, then the next scores, of half 0, then of half 1), which keeps
-            // one in its softmax while the other has the tensor cores; with a thread per half
+            // of its waits and operands, which come one after another. The buffers take strict
+            // turns (P V, then the next scores, of one, then of the other), which keeps one
+            // in its softmax while the other has the tensor cores; with a thread per buffer
             // they fall into step and both wait for both.
             if (elect_one()) {
                 constexpr uint32_t iS = tc_idesc_bf16(kRows, kRows, false);
@@ -758,7 +753,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const uint32_t v_ring = (uint32_t)tc_desc(ring, COL);
                 uint32_t n_q = 0;             // segments
                 uint32_t slot = 0, phase = 0; // ring position
-                uint32_t np0 = 0, np1 = 0;    // products with V issued per half
+                uint32_t np = 0, used = 0;    // per buffer: parity of its products with V; any yet
                 auto ready = [&](uint32_t bar, uint32_t parity) {
                     if (!dead && !mbar_ready(bar, parity & 1u)) {
                         dead = true;
@@ -766,52 +761,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     }
                     return !dead;
                 };
-                // scores of half I against the K tile in slot ks: Q K^T. The half's previous
-                // P V must be done: it reads P where the scores go.
-                auto scores = [&](auto half, int q, uint32_t np, uint32_t ks, bool release, bool last) {
-                    constexpr int I = decltype(half)::value;
-                    const uint64_t k_desc = kHigh | (k_ring + ks * kSlotDesc);
-                    half_mask[I] = slot_mask[ks]; // (the softmax is done with the last one)
-                    mbar_arrive(s_full + 8 * I);
-                    if (np && !ready(o_full + 8 * I, np - 1))
-                        return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * COL + (kk % 4) * 32) >> 4;
-                        tc_mma_ss(I * 128, kHigh | (q_desc + q * kSlotDesc + off), k_desc + off, iS,
-                                  kk > 0);
-                    }
-                    tc_commit(s_full + 8 * I);
-                    if (release)
-                        tc_commit(kv_empty + 8 * ks);
-                    if (last)
-                        tc_commit(q_empty);
-                };
-                // output of half I (+)= P V with the V tile in slot vs, in two parts
-                auto outputs = [&](auto half, uint32_t &np, uint32_t vs, uint32_t more,
-                                   bool release) {
-                    constexpr int I = decltype(half)::value;
-                    const uint64_t v_desc = kHigh | (v_ring + vs * kSlotDesc);
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        if (!ready(p_full + 16 * I + 8 * part, np))
-                            return;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = part * 4; kk < part * 4 + 4; ++kk)
-                            tc_mma_ts(256 + I * 128, I * 128 + 8 * kk, v_desc + kk * (2048 >> 4), iO,
-                                      kk > 0 ? 1 : more);
-                        if (part == 0)
-                            tc_commit(a_full + 8 * I);
-                    }
-                    tc_commit(o_full + 8 * I);
-                    if (release)
-                        tc_commit(kv_empty + 8 * vs);
-                    ++np;
-                };
-                using H0 = std::integral_constant<int, 0>;
-                using H1 = std::integral_constant<int, 1>;
                 // the next ring slot, once it is filled
                 auto take = [&](uint32_t &at) {
                     at = slot;
@@ -825,51 +774,69 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 while (walk.next(g)) {
                     const int n = g.j1 - g.j0;
                     const bool two = g.halves == 2;
-                    uint32_t ks, vs;
-                    if (!ready(q_full, n_q) || !take(ks))
+                    // Step k uses buffer k & 1: with two halves, half k & 1 and key tile k / 2;
+                    // with one, key tile k. Products of step k, then scores of step k + 2.
+                    const int steps = two ? 2 * n : n;
+                    uint32_t ks = 0, v0 = 0, v1 = 0; // slots of the K tile and of the last V tiles
+                    if (!ready(q_full, n_q))
                         break;
-                    scores(H0(), 0, np0, ks, !two, !two && n == 1);
-                    if (!take(vs))
-                        break;
-                    if (two) {
 #pragma unroll 1
-                        for (int jj = 0; jj < n && !dead; ++jj) {
-                            const bool more = jj + 1 < n;
-                            scores(H1(), 1, np1, ks, true, !more);
-                            outputs(H0(), np0, vs, jj > 0, false);
-                            if (more) {
-                                if (!take(ks))
+                    for (int k = -2; k < steps; ++k) {
+                        const uint32_t b = k & 1;
+                        const bool odd = b != 0, give = !two || odd; // a slot's last reader
+                        if (k >= 0) { // output (+)= P V, in two parts
+                            if (two ? !odd : k == n - 1) { // (else the scores' stage took it)
+                                if (!take(v0))
                                     break;
-                                scores(H0(), 0, np0, ks, false, false);
+                                v1 = v0;
                             }
-                            outputs(H1(), np1, vs, jj > 0, true);
-                            if (more && !take(vs))
+                            const uint32_t vs = odd ? v1 : v0;
+                            const uint64_t v_desc = kHigh | (v_ring + vs * kSlotDesc);
+                            const uint32_t tO = 256 + b * 128, tS = b * 128;
+                            const uint32_t more = k > 1;
+                            if (!ready(p_full + 16 * b, np >> b))
                                 break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < kRows / 32; ++kk)
+                                tc_mma_ts(tO, tS + 8 * kk, v_desc + kk * (2048 >> 4), iO,
+                                          kk > 0 ? 1 : more);
+                            tc_commit(a_full + 8 * b);
+                            if (!ready(p_full + 16 * b + 8, np >> b))
+                                break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = kRows / 32; kk < kRows / 16; ++kk)
+                                tc_mma_ts(tO, tS + 8 * kk, v_desc + kk * (2048 >> 4), iO, 1);
+                            tc_commit(o_full + 8 * b);
+                            if (give)
+                                tc_commit(kv_empty + 8 * vs);
+                            np ^= 1u << b;
                         }
-                    } else { // one half: tiles alternate between the two buffers
-                        if (n > 1) {
-                            if (!take(ks))
+                        if (k + 2 < steps) { // scores Q K^T of step k + 2
+                            if (!two && k + 2 > 0 && !take(odd ? v0 : v1)) // V of step k + 1
                                 break;
-                            scores(H1(), 0, np1, ks, true, n == 2);
-                        }
-#pragma unroll 1
-                        for (int jj = 0; jj < n && !dead; jj += 2) {
-                            outputs(H0(), np0, vs, jj > 0, true);
-                            if (jj + 1 == n || !take(vs))
+                            if (!(two && odd) && !take(ks))
                                 break;
-                            if (jj + 2 < n) {
-                                if (!take(ks))
-                                    break;
-                                scores(H0(), 0, np0, ks, true, jj + 3 == n);
+                            const uint64_t k_desc = kHigh | (k_ring + ks * kSlotDesc);
+                            const uint64_t a_desc = kHigh | (q_desc + (two ? b * kSlotDesc : 0));
+                            half_mask[b] = slot_mask[ks]; // (the softmax is done with the last one)
+                            mbar_arrive(s_full + 8 * b);
+                            // the buffer's last P V, which reads P where the scores go, must be done
+                            if ((used >> b & 1u) && !ready(o_full + 8 * b, (np >> b) ^ 1u))
+                                break;
+                            used |= 1u << b;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = ((kk / 4) * COL + (kk % 4) * 32) >> 4;
+                                tc_mma_ss(b * 128, a_desc + off, k_desc + off, iS, kk > 0);
                             }
-                            outputs(H1(), np1, vs, jj > 0, true);
-                            if (jj + 2 < n && !take(vs))
-                                break;
-                            if (jj + 3 < n) {
-                                if (!take(ks))
-                                    break;
-                                scores(H1(), 0, np1, ks, true, jj + 4 == n);
-                            }
+                            tc_commit(s_full + 8 * b);
+                            if (give)
+                                tc_commit(kv_empty + 8 * ks);
+                            if (k + 3 == steps)
+                                tc_commit(q_empty);
                         }
                     }
                     if (dead)
