@@ -66,7 +66,7 @@ struct CrossParams {
     int64_t num_blocks;
     int32_t num_seqs;
     int32_t n_kv;
-    int32_t g;
+    int32_t log2_g; // of the query heads per kv head
     int32_t max_blocks;
     int32_t num_ctas;
     float scale_log2;
@@ -93,7 +93,7 @@ __device__ __forceinline__ Seq load_seq(const CrossParams &p, int b, bool report
     s.q0 = q_ok ? q0 : 0;
     s.nq = q_ok ? q1 - q0 : 0;
     s.tiles = (int32_t)(((int64_t)s.ctx + kRows - 1) / kRows);
-    s.units = (int32_t)(((int64_t)s.nq * p.g + kUnitRows - 1) / kUnitRows);
+    s.units = (int32_t)((((int64_t)s.nq << p.log2_g) + kUnitRows - 1) / kUnitRows);
     return s;
 }
 
@@ -109,47 +109,52 @@ struct Segment {
     bool whole;
 };
 
+// Where a CTA's range of the line starts.
+struct Start {
+    int32_t b, kvh, qt, j; // sequence, kv head, unit of that head, key tile
+};
+
+// The segments of positions [lo, hi) of the line, one after another.
 struct Walk {
     const CrossParams &p;
-    int64_t lo, hi, pos;
-    int b;
-    int64_t vb; // position of sequence b's first item
+    int64_t pos, hi;
+    bool leading;
+    Start at;
     Seq s;
 
-    __device__ Walk(const CrossParams &p_, int64_t lo_, int64_t hi_, int b_, int64_t vb_)
-        : p(p_), lo(lo_), hi(hi_), pos(lo_), b(b_), vb(vb_)
+    __device__ Walk(const CrossParams &p_, int64_t lo, int64_t hi_, Start at_)
+        : p(p_), pos(lo), hi(hi_), leading(true), at(at_), s(load_seq(p_, at_.b, false))
     {
-        if (pos < hi)
-            s = load_seq(p, b, false);
     }
 
     __device__ bool next(Segment &g)
     {
-        if (pos < hi) {
-            int64_t c = s.items(p.n_kv);
-            while (pos >= vb + c) { // (pos is below the line's end, so b stays in range)
-                vb += c;
-                s = load_seq(p, ++b, false);
-                c = s.items(p.n_kv);
+        if (pos >= hi)
+            return false;
+        if (!leading && at.qt == s.units) {
+            at.qt = 0;
+            if (++at.kvh == p.n_kv) {
+                at.kvh = 0;
+                do // (pos is below the line's end, so there is a sequence with items)
+                    s = load_seq(p, ++at.b, false);
+                while (s.tiles == 0 || s.units == 0);
             }
-            const int64_t head = (int64_t)s.tiles * s.units;
-            int64_t r = pos - vb;
-            g.kvh = (int)div_small(r, head);
-            r -= g.kvh * head;
-            const int64_t qt = div_small(r, s.tiles);
-            g.j0 = (int)(r - qt * s.tiles);
-            g.first_v = pos - g.j0;
-            const int64_t end = g.first_v + s.tiles;
-            g.j1 = hi >= end ? s.tiles : (int)(hi - g.first_v);
-            g.leading = pos == lo;
-            pos = end;
-            g.row0 = qt * kUnitRows;
-            g.rows = (int)min((int64_t)kUnitRows, (int64_t)s.nq * p.g - g.row0);
-            g.halves = g.rows > kRows ? 2 : 1;
-            g.whole = g.j0 == 0 && g.j1 == s.tiles;
-            return true;
         }
-        return false;
+        const int n = (int)min((int64_t)(s.tiles - at.j), hi - pos);
+        g.kvh = at.kvh;
+        g.j0 = at.j;
+        g.j1 = at.j + n;
+        g.first_v = pos - at.j;
+        g.row0 = (int64_t)at.qt * kUnitRows;
+        g.rows = (int)min((int64_t)kUnitRows, ((int64_t)s.nq << p.log2_g) - g.row0);
+        g.halves = g.rows > kRows ? 2 : 1;
+        g.whole = g.j0 == 0 && g.j1 == s.tiles;
+        g.leading = leading;
+        leading = false;
+        pos += n;
+        at.j = 0;
+        ++at.qt;
+        return true;
     }
 };
 
@@ -342,8 +347,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                    p_full = s_full + 16 /* [half][part] */, o_full = p_full + 32,
                    a_full = o_full + 16, drained = a_full + 16, raw_full = drained + 8,
                    raw_empty = raw_full + 8 * L::RAWS;
-    // misc: [0] tensor memory base (0), [1] merge flag, [2..3] start sequence and
-    // position, [8..] bad-block masks per slot, [16..17] per half, [18..23] blocks of
+    // misc: [0] tensor memory base (0), [1] merge flag, [4..7] the range's start,
+    // [8..] bad-block masks per slot, [16..17] per half, [18..23] blocks of
     // the tiles of codes, [24..] scan
     int32_t *misc = reinterpret_cast<int32_t *>(smem + L::kOffMisc);
     volatile int32_t *slot_mask = misc + 8;
@@ -353,7 +358,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     auto record = [&](int64_t i) { return p.records + i * RECORD; };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n_h = p.n_kv * p.g;
+    const int n_h = p.n_kv << p.log2_g, g_mask = (1 << p.log2_g) - 1;
 
     // ---- this CTA's range of the line
     int64_t total;
@@ -392,8 +397,11 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         break;
                     v += c;
                 }
-                misc[2] = b;
-                *reinterpret_cast<int64_t *>(misc + 4) = v;
+                const Seq q = load_seq(p, b, false);
+                const int64_t head = (int64_t)q.tiles * q.units, in = lo - v;
+                const int64_t kvh = in / head, r = in - kvh * head, qt = r / q.tiles;
+                *reinterpret_cast<Start *>(misc + 4) = {b, (int32_t)kvh, (int32_t)qt,
+                                                        (int32_t)(r - qt * q.tiles)};
             }
         }
     }
@@ -439,7 +447,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = 0;
-    Walk walk(p, lo, hi, misc[2], *reinterpret_cast<int64_t *>(misc + 4));
+    Walk walk(p, lo, hi, *reinterpret_cast<const Start *>(misc + 4));
     Segment g;
     bool dead = false; // a wait gave up: no more waits, no more copies or products
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -606,8 +614,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             const int r = two ? half * kRows + row : row; // row within the unit
             const bool live = r < g.rows;
             const int64_t prow = g.row0 + r; // packed row of (sequence, kv head)
-            const int64_t t = prow / p.g, h = prow - t * p.g;
-            __nv_bfloat16 *o_row = p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D;
+            __nv_bfloat16 *o_row =
+                p.out + ((walk.s.q0 + (prow >> p.log2_g)) * n_h + (g.kvh << p.log2_g) +
+                         (prow & g_mask)) * D;
             float *rec = record((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1));
             // 32 outputs from column c on, of a row whose weights sum to l
             auto emit = [&](int c, const float (&o)[32], float inv) {
@@ -723,9 +732,11 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 for (int e = 0; e < 2; ++e) {
                     const float L = st[e].l, inv = L > 0.f || L != L ? 1.f / L : 0.f;
                     const float *o = st[e].o;
-                    const int64_t pr = g.row0 + rr[e], t = pr / p.g, h = pr - t * p.g;
+                    const int64_t pr = g.row0 + rr[e];
                     *reinterpret_cast<uint4 *>(
-                        p.out + ((walk.s.q0 + t) * n_h + g.kvh * p.g + h) * D + 8 * d8[e]) =
+                        p.out +
+                        ((walk.s.q0 + (pr >> p.log2_g)) * n_h + (g.kvh << p.log2_g) +
+                         (pr & g_mask)) * D + 8 * d8[e]) =
                         make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv),
                                    pack_bf16x2(o[2] * inv, o[3] * inv),
                                    pack_bf16x2(o[4] * inv, o[5] * inv),
@@ -857,7 +868,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             const uint32_t full0 = KIND ? raw_full : kv_full, empty0 = KIND ? raw_empty : kv_empty;
             while (walk.next(g) && !dead) {
                 const int nblk = (int)(((int64_t)walk.s.ctx + kBlockTokens - 1) / kBlockTokens);
-                const int32_t *table = p.block_tables + (int64_t)walk.b * p.max_blocks;
+                const int32_t *table = p.block_tables + (int64_t)walk.at.b * p.max_blocks;
                 for (int j = g.j0; j < g.j1; ++j) {
                     // lanes 0-7 (and their copies): the tile's eight blocks
                     const int blk = j * kTileBlocks + (lane & 7);
@@ -932,11 +943,12 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                             break;
                         if (elect_one()) {
                             mbar_arrive_expect_tx(q_full, (uint32_t)(g.halves * TILE));
-                            const int32_t t0 = (int32_t)(walk.s.q0 + g.row0 / p.g);
+                            const int32_t t0 = (int32_t)(walk.s.q0 + (g.row0 >> p.log2_g));
                             for (int i = 0; i < g.halves; ++i)
                                 for (int c = 0; c < HALVES; ++c)
                                     tma_load_3d(sbase + i * TILE + c * COL, &tmQ, c * 64,
-                                                g.kvh * p.g, t0 + i * (kRows / p.g), q_full);
+                                                g.kvh << p.log2_g, t0 + i * (kRows >> p.log2_g),
+                                                q_full);
                         }
                         __syncwarp();
                         ++n_q;
@@ -1075,7 +1087,7 @@ cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
     p.num_blocks = a.num_blocks;
     p.num_seqs = a.num_seqs;
     p.n_kv = a.n_kv;
-    p.g = a.g;
+    p.log2_g = a.g == 1 ? 0 : a.g == 2 ? 1 : a.g == 4 ? 2 : a.g == 8 ? 3 : 4;
     p.max_blocks = a.max_blocks;
     p.num_ctas = a.num_ctas;
     p.scale_log2 = a.scale_log2;
