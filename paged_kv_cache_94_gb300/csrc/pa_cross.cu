@@ -316,15 +316,31 @@ __device__ __forceinline__ uint32_t code4_bf2(uint32_t a, uint32_t b)
     return sub_bf16x2((t & 0x000f000fu) | 0x43004300u, 0x43084308u);
 }
 
-// mbar_wait with its slow path out of line: the common case, a barrier that is
-// ready or nearly so, stays a few instructions.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity)
+// mbar_wait whose polling is a few instructions: unrolled, as the compiler would, the
+// waiting warps' polls push the working ones' code out of the instruction cache.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity)
 {
-    return mbar_wait(bar, parity);
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (i % 64 == 0 && global_timer_ns() - t0 > 1000000000ull)
+            return false; // about a second: give up, as mbar_wait does
+    }
+}
+
+// The same with the polling out of line, for the thread that issues the matrix
+// instructions: its waits are mostly over when it comes to them.
+__device__ __noinline__ bool mbar_poll_slow(uint32_t bar, uint32_t parity)
+{
+    return mbar_poll(bar, parity);
 }
 __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity)
 {
-    return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity);
+    return mbar_try_wait(bar, parity) || mbar_poll_slow(bar, parity);
 }
 
 template <int D, int KIND>
@@ -451,7 +467,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     Segment g;
     bool dead = false; // a wait gave up: no more waits, no more copies or products
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, parity & 1u))) {
+        if (!dead && !__all_sync(0xffffffffu, mbar_poll(bar, parity & 1u))) {
             dead = true;
             if (lane == 0)
                 flag_error(p.dev_status, PA_DEV_TIMEOUT_BIT);
@@ -856,7 +872,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
                 if (dead) { // let what was issued finish (bounded) before the memory goes
                     tc_commit(drained);
-                    mbar_wait(drained, 0);
+                    mbar_poll(drained, 0);
                 }
             }
             __syncwarp();
@@ -957,9 +973,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
             if (dead) { // copies in flight land (bounded) before the memory goes
                 for (uint32_t n = n_kv > RING ? n_kv - RING : 0; n < n_kv; ++n)
-                    mbar_wait(full0 + 8 * (n % RING), (n / RING) & 1u);
+                    mbar_poll(full0 + 8 * (n % RING), (n / RING) & 1u);
                 if (n_q)
-                    mbar_wait(q_full, (n_q - 1) & 1u);
+                    mbar_poll(q_full, (n_q - 1) & 1u);
             }
         } else if constexpr (KIND != 0) {
             // ======================================================= codes into bf16
