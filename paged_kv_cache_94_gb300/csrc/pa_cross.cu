@@ -38,6 +38,8 @@
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
 
+#include <type_traits>
+
 namespace pa {
 namespace {
 
@@ -249,6 +251,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                  "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4])
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
                  : "memory");
 }
 
@@ -980,8 +990,17 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         } else if constexpr (KIND != 0) {
             // ======================================================= codes into bf16
             constexpr int CPR = L::ROWB / 16; // 16-byte chunks per row
-            constexpr int CHUNKS = kRows * CPR, CONV = kConvWarps * 32;
+            constexpr int CONV = kConvWarps * 32, STEP = CONV / CPR;
+            static_assert(STEP % 8 == 0, "rows of one thread lie alike in the swizzle");
             const int t = tid - (kCopyWarp + 1) * 32;
+            // where the thread's chunk of a row goes: 16-byte chunks of the row's bf16 values
+            const int flip = KIND == 1 && CPR == 8 ? (t % CPR) >> 2 : 0;
+            uint32_t at[4];
+#pragma unroll
+            for (int i = 0; i < (KIND == 1 ? 2 : 4); ++i) {
+                const int oc = KIND == 1 ? 2 * (t % CPR) + (i ^ flip) : 4 * (t % CPR) + i;
+                at[i] = (oc / 8) * COL + (((oc % 8) ^ (t / CPR & 7)) << 4);
+            }
             uint32_t n_kv = 0, n_tile = 0;
             while (walk.next(g) && !dead) {
                 for (int j = g.j0; j < g.j1 && !dead; ++j, ++n_tile) {
@@ -1008,40 +1027,42 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                             sc[t] = present(t) ? in[t] * p.scale_log2 : 0.f;
                             sc[kRows + t] = present(t) ? in[kRows + t] : 0.f;
                         }
+                        // Chunk t + i * CONV of the tile: its row moves by STEP, a multiple of the
+                        // swizzle's eight, so the addresses move by constants.
+                        auto convert = [&](auto checked) {
+                            uint32_t in = smem_u32(raw) + 16 * t, out = dst + t / CPR * 128;
 #pragma unroll 1 // (unrolled, its instructions push the other warps' out of the cache)
-                        for (int c = t; c < CHUNKS; c += CONV) {
-                            const int r = c / CPR, cr = c % CPR;
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (present(r))
-                                x = *reinterpret_cast<const uint4 *>(raw + 16 * c);
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            // 16-byte chunk oc of the row's bf16 values
-                            auto put = [&](int oc, uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
-                                sts128(dst + (oc / 8) * COL + r * 128 + (((oc % 8) ^ (r & 7)) << 4),
-                                       a, b, d, e);
-                            };
-                            if constexpr (KIND == 1) {
-                                // (a row's second 64 columns take its chunks in the other order: the
-                                // eight threads of a row then write to different banks)
-                                const int flip = CPR == 8 ? cr >> 2 : 0;
+                            for (int r = t / CPR; r < kRows; r += STEP) {
+                                uint32_t w[4];
+                                lds128(in, w);
+                                // rows that are not there are zero (INT4: 8 is code 0)
+                                if (checked && !present(r))
+                                    w[0] = w[1] = w[2] = w[3] = 0;
+                                if constexpr (KIND == 1) {
+                                    // (a row's second 64 columns take its chunks in the other
+                                    // order: a row's eight threads then write to different banks)
+                                    const uint32_t a0 = flip ? w[2] : w[0], a1 = flip ? w[3] : w[1];
+                                    const uint32_t b0 = flip ? w[0] : w[2], b1 = flip ? w[1] : w[3];
+                                    sts128(out + at[0], code8_bf2<0x4140>(a0), code8_bf2<0x4342>(a0),
+                                           code8_bf2<0x4140>(a1), code8_bf2<0x4342>(a1));
+                                    sts128(out + at[1], code8_bf2<0x4140>(b0), code8_bf2<0x4342>(b0),
+                                           code8_bf2<0x4140>(b1), code8_bf2<0x4342>(b1));
+                                } else {
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const bool up = i ^ flip;
-                                    const uint32_t a = up ? w[2] : w[0], b = up ? w[3] : w[1];
-                                    put(2 * cr + up, code8_bf2<0x4140>(a), code8_bf2<0x4342>(a),
-                                        code8_bf2<0x4140>(b), code8_bf2<0x4342>(b));
+                                    for (int i = 0; i < 4; ++i) {
+                                        const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
+                                        sts128(out + at[i], code4_bf2<0>(a, b), code4_bf2<1>(a, b),
+                                               code4_bf2<2>(a, b), code4_bf2<3>(a, b));
+                                    }
                                 }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
-                                    // (a row without codes is zero, not minus eight)
-                                    const uint32_t z = present(r) ? 0xffffffffu : 0u;
-                                    put(4 * cr + i, code4_bf2<0>(a, b) & z, code4_bf2<1>(a, b) & z,
-                                        code4_bf2<2>(a, b) & z, code4_bf2<3>(a, b) & z);
-                                }
+                                in += 16 * CONV;
+                                out += STEP * 128;
                             }
-                        }
+                        };
+                        if (valid == kRows && (mask & 0xff) == 0xff)
+                            convert(std::false_type());
+                        else
+                            convert(std::true_type());
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
