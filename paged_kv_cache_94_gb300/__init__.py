@@ -474,24 +474,69 @@ def pa_decode_mq(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 
 _NO_SWITCH = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(t: torch.Tensor, stream):
-    """Context with t's device current and, where a stream is given, that stream:
-    what a call allocates then belongs to the stream that uses it."""
+def _on(device, stream):
+    """Context with the tensors' device current and, where a stream is given, that
+    stream: what a call allocates then belongs to the stream that uses it."""
     if stream is not None:
-        if stream.device != t.device:
+        if stream.device != device:
             raise ValueError("stream and tensors are on different devices")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
     return _NO_SWITCH
 
 
-def _same_device(t: torch.Tensor, **others) -> None:
-    for name, o in others.items():
-        if o is not None and o.device != t.device:
-            raise ValueError(f"{name} is on {o.device}, not on {t.device}")
+def _stream_handle(device) -> int:
+    """The current stream of `device` as the C ABI takes it."""
+    return (_raw_stream(device.index) if _raw_stream is not None
+            else torch.cuda.current_stream(device).cuda_stream)
+
+
+def _take(name: str, t: torch.Tensor, dtype, device) -> int:
+    """The device pointer of a checked argument: a contiguous CUDA tensor of that
+    dtype on that device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or \
+            not t.is_contiguous():
+        _need_cuda(name, t, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _opt(name: str, t: Optional[torch.Tensor], dtype, device):
+    return None if t is None else _take(name, t, dtype, device)
+
+
+_GEOMS: dict = {}
+
+
+def _pool(k_cache, v_cache, k_scale, v_scale, n_h, device):
+    """Geometry of a pool and the pointers of its K, V and scales, checked."""
+    _need_cuda("k_cache", k_cache)
+    shape = k_cache.shape
+    key = (shape, k_cache.dtype, n_h)
+    g = _GEOMS.get(key)
+    if g is None:
+        g = geometry(k_cache, shape[1] if n_h is None and len(shape) == 4 else n_h)
+        _GEOMS[key] = g
+    kp = _take("k_cache", k_cache, k_cache.dtype, device)
+    vp = _take("v_cache", v_cache, k_cache.dtype, device)
+    if v_cache.shape != shape:
+        raise ValueError("v_cache must have the shape of k_cache")
+    if g.kv_dtype == PA_KV_BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale, v_scale: a bf16 pool has no scales")
+        return g, kp, vp, None, None
+    for nm, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if s is None:
+            raise ValueError(f"{nm} is required for an int8/int4 pool")
+        if s.shape != shape[:3]:
+            raise ValueError(f"{nm} must be [num_blocks, n_kv, block_size]")
+    return (g, kp, vp, _take("k_scale", k_scale, torch.float32, device),
+            _take("v_scale", v_scale, torch.float32, device))
 
 
 _STREAM_WS: dict = {}
@@ -506,7 +551,7 @@ def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) 
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws[:counters].zero_()
         return ws
-    key = (kind, device.index, torch.cuda.current_stream().cuda_stream)
+    key = (kind, device.index, _stream_handle(device))
     with _WS_LOCK:
         ent = _STREAM_WS.get(key)
         if ent is None or ent[0].numel() < nbytes:
@@ -517,17 +562,15 @@ def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) 
         return ent[0]
 
 
-def _check_quant(g: pa_geom, k_scale, v_scale, shape) -> None:
-    for nm, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if g.kv_dtype == PA_KV_BF16:
-            if s is not None:
-                raise ValueError(f"{nm}: a bf16 pool has no scales")
-            continue
-        if s is None:
-            raise ValueError(f"{nm} is required for an int8/int4 pool")
-        _need_cuda(nm, s, torch.float32)
-        if s.shape != shape[:3]:
-            raise ValueError(f"{nm} must be [num_blocks, n_kv, block_size]")
+def _issue(fn, args, stream_index: int, what: str, result, device, stream, keep, prepare: bool):
+    """Run a marshalled call on the current stream, or hand it out prepared."""
+    if prepare:
+        return Prepared(fn, args, stream_index, what, result, stream, keep)
+    args[stream_index] = _stream_handle(device)
+    st = fn(*args)
+    if st != 0:
+        raise PAError(st, what)
+    return result
 
 
 def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -546,59 +589,46 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     place). Entries at and behind a context's end are not written. Everything
     else, and the result, as pa_decode."""
     _need_cuda("q", q, torch.bfloat16)
-    _need_cuda("k_cache", k_cache)
-    _need_cuda("v_cache", v_cache, k_cache.dtype)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
-    _need_cuda("mass", mass, torch.float32)
-    if mass_out is None:
-        mass_out = mass
-    else:
-        _need_cuda("mass_out", mass_out, torch.float32)
+    dev = q.device
     if q.dim() != 3 or block_tables.dim() != 2:
         raise ValueError("q must be [num_seqs, n_h, d_h], block_tables [num_seqs, max_blocks]")
     B, n_h, d = q.shape
-    g = geometry(k_cache, n_h)
-    mb = block_tables.shape[1]
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("v_cache must have the shape of k_cache")
-    if d != g.d_h or block_tables.shape[0] != B or context_lens.shape != (B,):
+    tables, mb = block_tables.shape
+    g, kp, vp, ks, vs = _pool(k_cache, v_cache, k_scale, v_scale, n_h, dev)
+    if d != g.d_h or tables != B or context_lens.shape != (B,):
         raise ValueError("q, block_tables, context_lens disagree on num_seqs or d_h")
+    if mass_out is None:
+        mass_out = mass
     if mass.shape != (B, g.n_kv, mb * 16) or mass_out.shape != mass.shape:
         raise ValueError("mass, mass_out must be [num_seqs, n_kv, max_blocks * 16]")
-    _check_quant(g, k_scale, v_scale, k_cache.shape)
     if out is not None:
         _need_cuda("out", out, torch.bfloat16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-    if workspace is not None:
-        _need_cuda("workspace", workspace)
-    if dev_status is not None:
-        _need_cuda("dev_status", dev_status, torch.int32)
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, mass=mass, mass_out=mass_out, out=out, k_scale=k_scale,
-                 v_scale=v_scale, workspace=workspace, dev_status=dev_status)
-    with _on(q, stream):
+    num_ctas = int(num_ctas)
+    args = [q.data_ptr(), kp, vp, ks, vs,
+            _take("block_tables", block_tables, torch.int32, dev), mb,
+            _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None,
+            _take("mass", mass, torch.float32, dev),
+            _take("mass_out", mass_out, torch.float32, dev), None, 0, g,
+            _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
+    with _on(dev, stream):
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
-            key = ("mass", q.device.index, g.num_blocks, n_h, g.n_kv, d, g.kv_dtype, B, mb, num_ctas)
+            key = ("mass", dev.index, g.num_blocks, n_h, g.n_kv, d, g.kv_dtype, B, mb, num_ctas)
             nbytes = _WS_SIZES.get(key)
             if nbytes is None:
-                nbytes = _lib().pa_decode_mass_workspace_size(g, B, mb, int(num_ctas))
+                nbytes = _lib().pa_decode_mass_workspace_size(g, B, mb, num_ctas)
                 if nbytes == 0 and B > 0:
                     raise PAError(-4, "pa_decode_mass_workspace_size")
                 _WS_SIZES[key] = nbytes
-            workspace = _stream_workspace("mass", nbytes, _counter_bytes(g, B), q.device,
-                                          prepare)
-        call = Prepared(_lib().pa_decode_mass,
-                        [_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                         _ptr(block_tables), mb, _ptr(context_lens), B, float(scale), _ptr(out),
-                         _ptr(mass), _ptr(mass_out), _ptr(workspace),
-                         workspace.numel() * workspace.element_size(), g, _ptr(dev_status), None,
-                         int(num_ctas)],
-                        17, "pa_decode_mass", out, stream, workspace)
-        return call if prepare else call()
+            workspace = _stream_workspace("mass", nbytes, _counter_bytes(g, B), dev, prepare)
+        args[10] = _take("out", out, torch.bfloat16, dev)
+        args[13] = _take("workspace", workspace, workspace.dtype, dev)
+        args[14] = workspace.numel() * workspace.element_size()
+        return _issue(_lib().pa_decode_mass, args, 17, "pa_decode_mass", out, dev, stream,
+                      workspace, prepare)
 
 
 def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tensor,
@@ -616,54 +646,42 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
     are left as they were (in a new out: not initialised). The pool (bf16, INT8,
     INT4), its scales and tables are pa_decode's."""
     _need_cuda("q", q, torch.bfloat16)
-    _need_cuda("cu_q", cu_q, torch.int32)
-    _need_cuda("k_cache", k_cache)
-    _need_cuda("v_cache", v_cache, k_cache.dtype)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
+    dev = q.device
     if q.dim() != 3 or block_tables.dim() != 2:
         raise ValueError("q must be [num_q, n_h, d_h], block_tables [num_seqs, max_blocks]")
     T, n_h, d = q.shape
     B, mb = block_tables.shape
-    g = geometry(k_cache, n_h)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("v_cache must have the shape of k_cache")
+    g, kp, vp, ks, vs = _pool(k_cache, v_cache, k_scale, v_scale, n_h, dev)
     if d != g.d_h or context_lens.shape != (B,) or cu_q.shape != (B + 1,):
         raise ValueError("q, cu_q, block_tables, context_lens disagree on num_seqs or d_h")
-    _check_quant(g, k_scale, v_scale, k_cache.shape)
     if out is not None:
         _need_cuda("out", out, torch.bfloat16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-    if workspace is not None:
-        _need_cuda("workspace", workspace)
-    if dev_status is not None:
-        _need_cuda("dev_status", dev_status, torch.int32)
-    _same_device(q, cu_q=cu_q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, out=out, k_scale=k_scale, v_scale=v_scale,
-                 workspace=workspace, dev_status=dev_status)
-    with _on(q, stream):
+    num_ctas = int(num_ctas)
+    args = [q.data_ptr(), T, _take("cu_q", cu_q, torch.int32, dev), kp, vp, ks, vs,
+            _take("block_tables", block_tables, torch.int32, dev), mb,
+            _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None, None, 0,
+            g, _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
+    with _on(dev, stream):
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
-            key = ("cross", q.device.index, d, num_ctas)
+            key = ("cross", dev.index, d, num_ctas)
             nbytes = _WS_SIZES.get(key)
             if nbytes is None:
-                nbytes = _lib().pa_cross_workspace_size(g, int(num_ctas))
+                nbytes = _lib().pa_cross_workspace_size(g, num_ctas)
                 if nbytes == 0:
                     raise PAError(-4, "pa_cross_workspace_size")
                 _WS_SIZES[key] = nbytes
-            # (one counter per CTA in front of at least 2 * 256 * (d + 2) floats per CTA)
+            # (one counter per CTA in front of 2 * 256 * (d + 2) floats per CTA)
             counters = (nbytes // (512 * (d + 2) * 4) * 4 + 255) // 256 * 256
-            workspace = _stream_workspace("cross", nbytes, counters, q.device, prepare)
-        call = Prepared(_lib().pa_cross_attention,
-                        [_ptr(q), T, _ptr(cu_q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                         _ptr(v_scale), _ptr(block_tables), mb, _ptr(context_lens), B,
-                         float(scale), _ptr(out), _ptr(workspace),
-                         workspace.numel() * workspace.element_size(), g, _ptr(dev_status), None,
-                         int(num_ctas)],
-                        17, "pa_cross_attention", out, stream, workspace)
-        return call if prepare else call()
+            workspace = _stream_workspace("cross", nbytes, counters, dev, prepare)
+        args[12] = _take("out", out, torch.bfloat16, dev)
+        args[13] = _take("workspace", workspace, workspace.dtype, dev)
+        args[14] = workspace.numel() * workspace.element_size()
+        return _issue(_lib().pa_cross_attention, args, 17, "pa_cross_attention", out, dev, stream,
+                      workspace, prepare)
 
 
 def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int, recent: int = 0,
@@ -676,7 +694,7 @@ def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int,
     float32 [B, n_kv, max_tokens]; ties to the lowest index).
     -> (keep int32 [B, n_kv, budget], ascending, then -1; keep_lens int32 [B])."""
     _need_cuda("mass", mass, torch.float32)
-    _need_cuda("context_lens", context_lens, torch.int32)
+    dev = mass.device
     if mass.dim() != 3 or context_lens.shape != mass.shape[:1]:
         raise ValueError("mass must be [num_seqs, n_kv, max_tokens], context_lens [num_seqs]")
     B, n_kv, tokens = mass.shape
@@ -684,24 +702,20 @@ def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int,
     if budget <= 0 or not 0 <= recent <= budget:
         raise ValueError("budget must be > 0 and recent within 0 .. budget")
     for nm, t, shape in (("keep", keep, (B, n_kv, budget)), ("keep_lens", keep_lens, (B,))):
-        if t is not None:
-            _need_cuda(nm, t, torch.int32)
-            if t.shape != shape:
-                raise ValueError(f"{nm} must be {list(shape)}")
-    if dev_status is not None:
-        _need_cuda("dev_status", dev_status, torch.int32)
-    _same_device(mass, context_lens=context_lens, keep=keep, keep_lens=keep_lens,
-                 dev_status=dev_status)
-    with _on(mass, stream):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{nm} must be {list(shape)}")
+    ctx = _take("context_lens", context_lens, torch.int32, dev)
+    status = _opt("dev_status", dev_status, torch.int32, dev)
+    with _on(dev, stream):
         if keep is None:
-            keep = torch.empty((B, n_kv, budget), dtype=torch.int32, device=mass.device)
+            keep = torch.empty((B, n_kv, budget), dtype=torch.int32, device=dev)
         if keep_lens is None:
-            keep_lens = torch.empty(B, dtype=torch.int32, device=mass.device)
-        call = Prepared(_lib().pa_evict_select,
-                        [_ptr(mass), tokens, _ptr(context_lens), B, n_kv, budget, recent,
-                         _ptr(keep), _ptr(keep_lens), _ptr(dev_status), None],
-                        10, "pa_evict_select", (keep, keep_lens), stream)
-        return call if prepare else call()
+            keep_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        args = [mass.data_ptr(), tokens, ctx, B, n_kv, budget, recent,
+                _take("keep", keep, torch.int32, dev),
+                _take("keep_lens", keep_lens, torch.int32, dev), status, None]
+        return _issue(_lib().pa_evict_select, args, 10, "pa_evict_select", (keep, keep_lens), dev,
+                      stream, None, prepare)
 
 
 def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -717,44 +731,31 @@ def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     max_blocks * 16], the kept tokens' masses go to mass_out [B, n_kv,
     new_blocks * 16], 0 behind them."""
     _need_cuda("k_cache", k_cache)
-    _need_cuda("v_cache", v_cache, k_cache.dtype)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("keep", keep, torch.int32)
-    _need_cuda("keep_lens", keep_lens, torch.int32)
-    _need_cuda("new_tables", new_tables, torch.int32)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("v_cache must have the shape of k_cache")
-    g = geometry(k_cache, n_h=k_cache.shape[1])
-    _check_quant(g, k_scale, v_scale, k_cache.shape)
+    dev = k_cache.device
+    g, kp, vp, ks, vs = _pool(k_cache, v_cache, k_scale, v_scale, None, dev)
     if block_tables.dim() != 2 or new_tables.dim() != 2 or keep.dim() != 3:
         raise ValueError("block_tables, new_tables must be [num_seqs, blocks], keep "
                          "[num_seqs, n_kv, budget]")
-    B, budget = keep.shape[0], keep.shape[2]
-    mb, nb = block_tables.shape[1], new_tables.shape[1]
-    if keep.shape[1] != g.n_kv or block_tables.shape[0] != B or new_tables.shape[0] != B or \
-            keep_lens.shape != (B,):
+    B, heads, budget = keep.shape
+    tables, mb = block_tables.shape
+    news, nb = new_tables.shape
+    if heads != g.n_kv or tables != B or news != B or keep_lens.shape != (B,):
         raise ValueError("keep, keep_lens and the tables disagree on num_seqs or n_kv")
     if (mass is None) != (mass_out is None):
         raise ValueError("mass and mass_out go together")
-    if mass is not None:
-        _need_cuda("mass", mass, torch.float32)
-        _need_cuda("mass_out", mass_out, torch.float32)
-        if mass.shape != (B, g.n_kv, mb * 16) or mass_out.shape != (B, g.n_kv, nb * 16):
-            raise ValueError("mass must be [num_seqs, n_kv, max_blocks * 16], mass_out "
-                             "[num_seqs, n_kv, new_blocks * 16]")
-    if dev_status is not None:
-        _need_cuda("dev_status", dev_status, torch.int32)
-    _same_device(k_cache, v_cache=v_cache, block_tables=block_tables, keep=keep,
-                 keep_lens=keep_lens, new_tables=new_tables, mass=mass, mass_out=mass_out,
-                 k_scale=k_scale, v_scale=v_scale, dev_status=dev_status)
-    with _on(k_cache, stream):
-        call = Prepared(_lib().pa_evict_compact,
-                        [_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                         _ptr(block_tables), mb, _ptr(keep), budget, _ptr(keep_lens),
-                         _ptr(new_tables), nb, B, _ptr(mass), _ptr(mass_out), g,
-                         _ptr(dev_status), None],
-                        16, "pa_evict_compact", None, stream)
-        return call if prepare else call()
+    if mass is not None and (mass.shape != (B, g.n_kv, mb * 16) or
+                             mass_out.shape != (B, g.n_kv, nb * 16)):
+        raise ValueError("mass must be [num_seqs, n_kv, max_blocks * 16], mass_out "
+                         "[num_seqs, n_kv, new_blocks * 16]")
+    args = [kp, vp, ks, vs, _take("block_tables", block_tables, torch.int32, dev), mb,
+            _take("keep", keep, torch.int32, dev), budget,
+            _take("keep_lens", keep_lens, torch.int32, dev),
+            _take("new_tables", new_tables, torch.int32, dev), nb, B,
+            _opt("mass", mass, torch.float32, dev), _opt("mass_out", mass_out, torch.float32, dev),
+            g, _opt("dev_status", dev_status, torch.int32, dev), None]
+    with _on(dev, stream):
+        return _issue(_lib().pa_evict_compact, args, 16, "pa_evict_compact", None, dev, stream,
+                      None, prepare)
 
 
 def pa_sink_write(k: torch.Tensor, v: torch.Tensor, seq_rows: torch.Tensor,
