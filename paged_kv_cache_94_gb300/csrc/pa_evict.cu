@@ -4,9 +4,10 @@
 //   k = min(n, budget), r = min(recent, k): tokens n - r .. n - 1, and of the
 //   m = n - r before them the k - r of largest mass, ties to the lowest index,
 //   in ascending order. The k - r th largest key (masses as unsigned integers
-//   in their order) is found digit by digit, 11 + 11 + 10 bits, from counts in
-//   shared memory; one more sweep counts what lies above it and writes the
-//   indices at their ranks. Ranks come from warp ballots and prefix sums, so
+//   in their order) is found from counts of its top 11 bits in shared memory (and
+//   of 11 more, and the last 10, where many keys share those), then by comparing
+//   the few keys of its bin with each other; one more sweep counts what lies above
+//   it and writes the indices at their ranks. Ranks come from warp ballots and prefix sums, so
 //   the result does not depend on any order of execution.
 //   A row is 4 n bytes, read once: latency-bound. So a long row is cut over a
 //   cluster of up to 8 CTAs (counts joined in the first one's shared memory) and
@@ -43,16 +44,22 @@ __device__ __forceinline__ uint32_t key_of(float x)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+constexpr int kFew = 512; // candidates that are ranked by comparing them with each other
+
 struct SelShared {
     int32_t hist[kBins];
     int32_t total[kBins]; // the cluster's counts (first CTA)
+    uint32_t few[kFew];   // the candidates' keys (first CTA)
+    int32_t n_few;
     int32_t warp_sum[kSelWarps];
-    int32_t digit, need;  // result of a digit's scan
+    uint32_t prefix;      // result of a step: the threshold's known bits,
+    int32_t need, left;   // tokens still wanted from its bin, tokens in the bin
     int32_t gt[kSelWarps], eq[kSelWarps];
     int32_t cta_gt, cta_eq;
 };
 
-template <bool CACHED>
+// CACHED: a thread keeps its keys in registers. CLUSTER: several CTAs per row.
+template <bool CACHED, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads)
 select_kernel(const float *__restrict__ mass, int64_t stride,
               const int32_t *__restrict__ context_lens, int n_kv, int budget, int recent,
@@ -60,7 +67,15 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
 {
     __shared__ SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int C = CLUSTER ? (int)cluster.num_blocks() : 1;
+    const int rank = CLUSTER ? (int)cluster.block_rank() : 0;
+    auto sync = [&]() {
+        if constexpr (CLUSTER)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+    auto of = [&](int q) { return CLUSTER ? cluster.map_shared_rank(&sh, q) : &sh; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t u = blockIdx.x / C; // b * n_kv + kv head
     const int b = (int)(u / n_kv);
@@ -105,9 +120,11 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
     auto sweep = [&](auto f) {
         if constexpr (CACHED) {
 #pragma unroll
-            for (int it = 0; it < kKeys; ++it)
-                if (it < rounds)
-                    f(it, keys[it], first + it * 32 < m);
+            for (int it = 0; it < kKeys; ++it) {
+                if (it >= rounds)
+                    break;
+                f(it, keys[it], first + it * 32 < m);
+            }
         } else {
             for (int it = 0; it < rounds; ++it) {
                 const bool in = first + (int64_t)it * 32 < m;
@@ -116,29 +133,35 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
         }
     };
 
+    // The `want`-th largest key: its top 11 bits from counts, then 11 more and the last 10
+    // while its bin holds too many keys to compare them all with each other.
     uint32_t prefix = 0;
-    int32_t need = want;
+    int32_t need = want, left = m;
     int top = 32; // bits [top, 32) of the threshold are known
+    auto in_bin = [&](uint32_t key) { return top == 32 || (key >> top) == (prefix >> top); };
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int bits = pass < 2 ? 11 : 10, low = top - bits;
-        for (int i = tid; i < kBins; i += kSelThreads)
-            sh.hist[i] = sh.total[i] = 0;
-        cluster.sync(); // the first CTA's totals are zero before anyone adds to them
+    while (top > 0 && left > kFew) {
+        const int bits = top > 10 ? 11 : 10, low = top - bits;
+        for (int i = tid; i < kBins; i += kSelThreads) {
+            sh.hist[i] = 0;
+            if (CLUSTER)
+                sh.total[i] = 0;
+        }
+        sync(); // (the first CTA's totals are zero before anyone adds to them)
         sweep([&](int, uint32_t key, bool in) {
-            if (in && (top == 32 || (key >> top) == (prefix >> top)))
+            if (in && in_bin(key))
                 atomicAdd(&sh.hist[(key >> low) & ((1u << bits) - 1)], 1);
         });
         __syncthreads();
-        int32_t *total = C == 1 ? sh.hist : cluster.map_shared_rank(sh.total, 0);
-        if (C > 1) {
+        if constexpr (CLUSTER) {
+            int32_t *total = of(0)->total;
             for (int i = tid; i < kBins; i += kSelThreads)
                 if (sh.hist[i])
                     atomicAdd(total + i, sh.hist[i]);
             cluster.sync();
         }
         if (rank == 0) { // the digit: counts from the top until `need` are covered
-            const int32_t *t = C == 1 ? sh.hist : sh.total;
+            const int32_t *t = CLUSTER ? sh.total : sh.hist;
             constexpr int PER = kBins / kSelThreads;
             int32_t c[PER], sum = 0;
 #pragma unroll
@@ -157,24 +180,54 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
                 sh.warp_sum[warp] = x;
             __syncthreads();
             int32_t before = x - sum;
-            for (int w = 0; w < warp; ++w)
-                before += sh.warp_sum[w];
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w)
+                before += w < warp ? sh.warp_sum[w] : 0;
             if (before < need && need <= before + sum) { // exactly one thread
                 int j = 0;
                 while (before + c[j] < need)
                     before += c[j++];
-                const int32_t digit = kBins - 1 - (tid * PER + j), left = need - before;
+                const uint32_t digit = kBins - 1 - (tid * PER + j);
                 for (int q = 0; q < C; ++q) {
-                    SelShared *s = cluster.map_shared_rank(&sh, q);
-                    s->digit = digit;
-                    s->need = left;
+                    SelShared *s = of(q);
+                    s->prefix = prefix | digit << low;
+                    s->need = need - before;
+                    s->left = c[j];
                 }
             }
         }
-        cluster.sync();
-        prefix |= (uint32_t)sh.digit << low;
+        sync();
+        prefix = sh.prefix;
         need = sh.need;
+        left = sh.left;
         top = low;
+    }
+    if (top > 0) { // few: the need-th largest of them by comparing all with all
+        if (tid == 0)
+            sh.n_few = 0;
+        sync();
+        SelShared *to = of(0);
+        sweep([&](int, uint32_t key, bool in) {
+            if (in && in_bin(key))
+                to->few[atomicAdd(&to->n_few, 1)] = key;
+        });
+        sync();
+        if (rank == 0 && tid < left) {
+            const uint32_t mine = sh.few[tid];
+            int32_t above = 0, same = 0;
+            for (int i = 0; i < left; ++i) {
+                above += sh.few[i] > mine;
+                same += sh.few[i] == mine;
+            }
+            if (above < need && need <= above + same) // one key (every thread that has it)
+                for (int q = 0; q < C; ++q) {
+                    of(q)->prefix = mine;
+                    of(q)->left = need - above;
+                }
+        }
+        sync();
+        prefix = sh.prefix;
+        need = sh.left;
     }
 
     // ranks: tokens above the threshold, and the first `need` of those equal to it
@@ -191,11 +244,12 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
     }
     __syncthreads();
     int32_t gt0 = 0, eq0 = 0; // before this warp
+#pragma unroll
     for (int w = 0; w < kSelWarps; ++w) {
         gt0 += w < warp ? sh.gt[w] : 0;
         eq0 += w < warp ? sh.eq[w] : 0;
     }
-    if (C > 1) {
+    if constexpr (CLUSTER) {
         if (tid == 0) {
             int32_t g = 0, e = 0;
             for (int w = 0; w < kSelWarps; ++w) {
@@ -207,8 +261,8 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
         }
         cluster.sync();
         for (int q = 0; q < rank; ++q) {
-            gt0 += *cluster.map_shared_rank(&sh.cta_gt, q);
-            eq0 += *cluster.map_shared_rank(&sh.cta_eq, q);
+            gt0 += of(q)->cta_gt;
+            eq0 += of(q)->cta_eq;
         }
     }
     const uint32_t below = (1u << lane) - 1;
@@ -221,7 +275,7 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
         gt0 += __popc(g);
         eq0 += __popc(e);
     });
-    if (C > 1)
+    if constexpr (CLUSTER)
         cluster.sync(); // no CTA leaves while another reads its shared memory
 }
 
@@ -331,10 +385,11 @@ cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cached ? select_kernel<true> : select_kernel<false>, mass,
-                              stride, context_lens, n_kv, budget, recent, keep, keep_lens,
-                              dev_status);
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    auto kernel = C > 1 ? cached ? select_kernel<true, true> : select_kernel<false, true>
+                        : cached ? select_kernel<true, false> : select_kernel<false, false>;
+    return cudaLaunchKernelEx(&cfg, kernel, mass, stride, context_lens, n_kv, budget, recent, keep,
+                              keep_lens, dev_status);
 }
 
 cudaError_t launch_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
