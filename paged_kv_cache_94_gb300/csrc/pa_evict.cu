@@ -4,15 +4,16 @@
 //   k = min(n, budget), r = min(recent, k): tokens n - r .. n - 1, and of the
 //   m = n - r before them the k - r of largest mass, ties to the lowest index,
 //   in ascending order. The k - r th largest key (masses as unsigned integers
-//   in their order) is found from counts of its top 11 bits in shared memory (and
-//   of 11 more, and the last 10, where many keys share those), then by comparing
-//   the few keys of its bin with each other; one more sweep counts what lies above
-//   it and writes the indices at their ranks. Ranks come from warp ballots and prefix sums, so
-//   the result does not depend on any order of execution.
+//   in their order) is found from counts over 2048 bins of the keys' range in
+//   shared memory, again over the bin that holds it while many do, then by
+//   comparing the few keys of its bin with each other; one more sweep counts what
+//   lies above it and writes the indices at their ranks. Ranks come from warp
+//   ballots and prefix sums, so the result does not depend on any order of
+//   execution.
 //   A row is 4 n bytes, read once: latency-bound. So a long row is cut over a
 //   cluster of up to 8 CTAs (counts joined in the first one's shared memory) and
-//   each thread keeps its keys in registers between the sweeps; rows too long
-//   for that read them again from L2.
+//   the keys stay in shared memory between the sweeps; rows too long for that
+//   read them again from L2.
 //
 // compact_kernel: row i of the new block table = row keep[i] of the old one,
 //   for K, V, their scales and the masses. Bound by HBM: each kept row is read
@@ -32,10 +33,11 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kKeys = 32; // keys a thread keeps in registers
+constexpr int kKeys = 48; // keys of a thread that fit in shared memory, two CTAs per SM
 
 // Masses as unsigned integers of the same order. -0 equals +0; NaN lies below
 // everything, so a token whose mass is not a number goes first.
+constexpr uint32_t kZeroKey = 0x80000000u;
 __device__ __forceinline__ uint32_t key_of(float x)
 {
     const uint32_t u = __float_as_uint(x + 0.f); // -0 + 0 = +0
@@ -52,15 +54,16 @@ struct SelShared {
     uint32_t few[kFew];   // the candidates' keys (first CTA)
     int32_t n_few;
     int32_t warp_sum[kSelWarps];
-    uint32_t prefix;      // result of a step: the threshold's known bits,
-    int32_t need, left;   // tokens still wanted from its bin, tokens in the bin
+    uint32_t low[kSelWarps], low_pos[kSelWarps], high[kSelWarps]; // least keys, greatest
+    uint32_t lo, hi;      // result of a step: the threshold's range,
+    int32_t need, left;   // its rank there, keys there
     int32_t gt[kSelWarps], eq[kSelWarps];
     int32_t cta_gt, cta_eq;
 };
 
-// CACHED: a thread keeps its keys in registers. CLUSTER: several CTAs per row.
+// CACHED: the keys stay in shared memory (each thread's own). CLUSTER: several CTAs per row.
 template <bool CACHED, bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 2)
 select_kernel(const float *__restrict__ mass, int64_t stride,
               const int32_t *__restrict__ context_lens, int n_kv, int budget, int recent,
               int32_t *__restrict__ keep, int32_t *__restrict__ keep_lens, int32_t *dev_status)
@@ -110,47 +113,76 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
     auto load = [&](int it) -> uint32_t { // (only called for tokens below m)
         return key_of(__ldg(row + first + (int64_t)it * 32));
     };
-    uint32_t keys[CACHED ? kKeys : 1];
+    extern __shared__ uint32_t keys[];
+    uint32_t *mine = keys + warp * rounds * 32 + lane;
     if constexpr (CACHED) {
-#pragma unroll
-        for (int it = 0; it < kKeys; ++it)
-            keys[it] = it < rounds && first + it * 32 < m ? load(it) : 0u;
+#pragma unroll 8
+        for (int it = 0; it < rounds; ++it)
+            mine[it * 32] = first + it * 32 < m ? load(it) : 0u;
     }
     // f(round, key, valid) over this thread's tokens, all lanes of a warp together
     auto sweep = [&](auto f) {
-        if constexpr (CACHED) {
-#pragma unroll
-            for (int it = 0; it < kKeys; ++it) {
-                if (it >= rounds)
-                    break;
-                f(it, keys[it], first + it * 32 < m);
-            }
-        } else {
-            for (int it = 0; it < rounds; ++it) {
-                const bool in = first + (int64_t)it * 32 < m;
-                f(it, in ? load(it) : 0u, in);
-            }
+#pragma unroll 4
+        for (int it = 0; it < rounds; ++it) {
+            const bool in = first + (int64_t)it * 32 < m;
+            f(it, CACHED ? mine[it * 32] : in ? load(it) : 0u, in);
         }
     };
 
-    // The `want`-th largest key: its top 11 bits from counts, then 11 more and the last 10
-    // while its bin holds too many keys to compare them all with each other.
-    uint32_t prefix = 0;
-    int32_t need = want, left = m;
-    int top = 32; // bits [top, 32) of the threshold are known
-    auto in_bin = [&](uint32_t key) { return top == 32 || (key >> top) == (prefix >> top); };
-#pragma unroll 1
-    while (top > 0 && left > kFew) {
-        const int bits = top > 10 ? 11 : 10, low = top - bits;
-        for (int i = tid; i < kBins; i += kSelThreads) {
-            sh.hist[i] = 0;
-            if (CLUSTER)
-                sh.total[i] = 0;
+    // The range of the keys: all, and of the masses above zero.
+    uint32_t lowest = 0xffffffffu, low_pos = 0xffffffffu, hi = 0;
+    sweep([&](int, uint32_t key, bool in) {
+        if (in) {
+            lowest = min(lowest, key);
+            low_pos = key > kZeroKey ? min(low_pos, key) : low_pos;
+            hi = max(hi, key);
         }
-        sync(); // (the first CTA's totals are zero before anyone adds to them)
+    });
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+    low_pos = __reduce_min_sync(0xffffffffu, low_pos);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        sh.low[warp] = lowest;
+        sh.low_pos[warp] = low_pos;
+        sh.high[warp] = hi;
+    }
+    if (tid == 0)
+        sh.n_few = 0;
+    for (int i = tid; i < kBins; i += kSelThreads)
+        sh.hist[i] = sh.total[i] = 0;
+    sync();
+    for (int i = lane; i < C * kSelWarps; i += 32) { // every warp joins all of the row's
+        SelShared *s = of(i / kSelWarps);
+        lowest = min(lowest, s->low[i % kSelWarps]);
+        low_pos = min(low_pos, s->low_pos[i % kSelWarps]);
+        hi = max(hi, s->high[i % kSelWarps]);
+    }
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+    low_pos = __reduce_min_sync(0xffffffffu, low_pos);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+
+    // The `want`-th largest key lies in [lo, hi] and is the need-th largest of the `left`
+    // keys there. Counts over up to 2048 equal bins of that range narrow it, first of the
+    // masses above zero (zeros would stretch the range over all the exponents), until few are
+    // left, which are compared with each other.
+    uint32_t lo = low_pos <= hi && m > kFew ? low_pos : lowest;
+    int32_t need = want, left = m;
+    bool clean = true; // the counts are zero
+#pragma unroll 1
+    while (left > kFew && (lo < hi || (clean && lo > lowest))) {
+        const int bits = 32 - __clz(hi - lo), shift = max(0, bits - 11);
+        if (!clean) {
+            for (int i = tid; i < kBins; i += kSelThreads) {
+                sh.hist[i] = 0;
+                if (CLUSTER)
+                    sh.total[i] = 0;
+            }
+            sync(); // (the first CTA's totals are zero before anyone adds to them)
+        }
+        clean = false;
         sweep([&](int, uint32_t key, bool in) {
-            if (in && in_bin(key))
-                atomicAdd(&sh.hist[(key >> low) & ((1u << bits) - 1)], 1);
+            if (in && key - lo <= hi - lo)
+                atomicAdd(&sh.hist[(key - lo) >> shift], 1);
         });
         __syncthreads();
         if constexpr (CLUSTER) {
@@ -160,7 +192,7 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
                     atomicAdd(total + i, sh.hist[i]);
             cluster.sync();
         }
-        if (rank == 0) { // the digit: counts from the top until `need` are covered
+        if (rank == 0) { // the bin: counts from the top until `need` are covered
             const int32_t *t = CLUSTER ? sh.total : sh.hist;
             constexpr int PER = kBins / kSelThreads;
             int32_t c[PER], sum = 0;
@@ -183,58 +215,66 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
 #pragma unroll
             for (int w = 0; w < kSelWarps; ++w)
                 before += w < warp ? sh.warp_sum[w] : 0;
-            if (before < need && need <= before + sum) { // exactly one thread
-                int j = 0;
-                while (before + c[j] < need)
-                    before += c[j++];
-                const uint32_t digit = kBins - 1 - (tid * PER + j);
+            const bool here = before < need && need <= before + sum; // in one thread at most
+            const bool below = tid == kSelThreads - 1 && before + sum < need;
+            if (here || below) { // `below`: among the masses that are not above zero
+                uint32_t new_lo = lowest, new_hi = lo - 1;
+                int32_t new_left = m - (before + sum), new_need = need - (before + sum);
+                if (here) {
+                    int j = 0;
+                    while (before + c[j] < need)
+                        before += c[j++];
+                    new_lo = lo + ((uint32_t)(kBins - 1 - (tid * PER + j)) << shift);
+                    new_hi = min(hi, new_lo + ((1u << shift) - 1));
+                    new_left = c[j];
+                    new_need = need - before;
+                }
                 for (int q = 0; q < C; ++q) {
                     SelShared *s = of(q);
-                    s->prefix = prefix | digit << low;
-                    s->need = need - before;
-                    s->left = c[j];
+                    s->lo = new_lo;
+                    s->hi = new_hi;
+                    s->need = new_need;
+                    s->left = new_left;
                 }
             }
         }
         sync();
-        prefix = sh.prefix;
+        lo = sh.lo;
+        hi = sh.hi;
         need = sh.need;
         left = sh.left;
-        top = low;
     }
-    if (top > 0) { // few: the need-th largest of them by comparing all with all
-        if (tid == 0)
-            sh.n_few = 0;
-        sync();
+    if (lo < hi) { // few: the need-th largest of them by comparing all with all
         SelShared *to = of(0);
         sweep([&](int, uint32_t key, bool in) {
-            if (in && in_bin(key))
+            if (in && key - lo <= hi - lo)
                 to->few[atomicAdd(&to->n_few, 1)] = key;
         });
         sync();
         if (rank == 0 && tid < left) {
-            const uint32_t mine = sh.few[tid];
+            const uint32_t own = sh.few[tid];
             int32_t above = 0, same = 0;
             for (int i = 0; i < left; ++i) {
-                above += sh.few[i] > mine;
-                same += sh.few[i] == mine;
+                above += sh.few[i] > own;
+                same += sh.few[i] == own;
             }
             if (above < need && need <= above + same) // one key (every thread that has it)
                 for (int q = 0; q < C; ++q) {
-                    of(q)->prefix = mine;
-                    of(q)->left = need - above;
+                    of(q)->lo = own;
+                    of(q)->need = need - above;
                 }
         }
         sync();
-        prefix = sh.prefix;
-        need = sh.left;
+        lo = sh.lo;
+        need = sh.need;
     }
+    const uint32_t threshold = lo;
 
     // ranks: tokens above the threshold, and the first `need` of those equal to it
     int32_t gt = 0, eq = 0;
     sweep([&](int, uint32_t key, bool in) {
-        gt += in && key > prefix;
-        eq += in && key == prefix;
+        gt += in && key > threshold;
+        eq += in && key == threshold;
     });
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -267,10 +307,10 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
     }
     const uint32_t below = (1u << lane) - 1;
     sweep([&](int it, uint32_t key, bool in) {
-        const uint32_t g = __ballot_sync(0xffffffffu, in && key > prefix);
-        const uint32_t e = __ballot_sync(0xffffffffu, in && key == prefix);
+        const uint32_t g = __ballot_sync(0xffffffffu, in && key > threshold);
+        const uint32_t e = __ballot_sync(0xffffffffu, in && key == threshold);
         const int32_t gb = gt0 + __popc(g & below), eb = eq0 + __popc(e & below);
-        if (in && (key > prefix || (key == prefix && eb < need)))
+        if (in && (key > threshold || (key == threshold && eb < need)))
             out[gb + min(eb, need)] = (int32_t)(first + (int64_t)it * 32);
         gt0 += __popc(g);
         eq0 += __popc(e);
@@ -374,7 +414,8 @@ cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t
         C *= 2;
     if (rows * C > INT32_MAX)
         return cudaErrorInvalidValue;
-    const bool cached = stride <= (int64_t)C * kSelThreads * kKeys;
+    const int64_t per_thread = (stride + (int64_t)C * kSelThreads - 1) / ((int64_t)C * kSelThreads);
+    const bool cached = per_thread <= kKeys;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kSelThreads);
@@ -388,6 +429,15 @@ cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t
     cfg.numAttrs = C > 1 ? 1 : 0;
     auto kernel = C > 1 ? cached ? select_kernel<true, true> : select_kernel<false, true>
                         : cached ? select_kernel<true, false> : select_kernel<false, false>;
+    if (cached)
+        cfg.dynamicSmemBytes = (size_t)per_thread * kSelThreads * sizeof(uint32_t);
+    if (cfg.dynamicSmemBytes > 16 * 1024) { // (with the static part, over the 48 KiB default at most)
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kKeys * kSelThreads * (int)sizeof(uint32_t));
+        if (e != cudaSuccess)
+            return e;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, mass, stride, context_lens, n_kv, budget, recent, keep,
                               keep_lens, dev_status);
 }

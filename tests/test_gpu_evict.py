@@ -232,18 +232,19 @@ def test_select_matches_the_plain_choice(tokens, budget, recent):
     check_select(mass, ctx, budget, recent)
 
 
-@pytest.mark.parametrize("tokens,budget", [(20000, 900), (60001, 30000), (140003, 16384)])
+@pytest.mark.parametrize("tokens,budget", [(20000, 900), (60001, 30000), (140003, 16384),
+                                           (200003, 70000)])
 def test_select_of_long_rows(tokens, budget):
-    """Rows over a cluster of CTAs, the longest not kept in registers."""
+    """Rows over a cluster of CTAs, the longest too long to be kept between the sweeps."""
     gen = torch.Generator().manual_seed(tokens)
     check_select(torch.exp(torch.randn(2, 1, tokens, generator=gen)), [tokens, tokens - 777],
                  budget, 100)
 
 
 def test_select_of_many_long_rows():
-    """More rows than SMs and too long for registers: one CTA a row, read again."""
+    """More rows than SMs and too long to be kept: one CTA a row, read again."""
     gen = torch.Generator().manual_seed(9)
-    check_select(torch.rand(80, 4, 16500, generator=gen), [16500 - b for b in range(80)], 50, 5)
+    check_select(torch.rand(80, 4, 24600, generator=gen), [24600 - b for b in range(80)], 50, 5)
 
 
 @pytest.mark.parametrize("case", ["equal", "zeros", "steps", "signs", "special"])
