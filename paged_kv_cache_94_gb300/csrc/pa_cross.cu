@@ -11,9 +11,9 @@
 // Split. The query rows of a kv head (tokens x the g heads that share it) are
 // packed: row t * g + h. A unit is (sequence, kv head, up to 256 packed rows),
 // one or two halves of 128 rows = one tensor-core tile each; its items are
-// the 128-key tiles of the context. Items lie on one line (one or two halves
-// take about as long) and CTA c of G takes [c W / G, (c + 1) W / G) of it, so any
-// mix of lengths is balanced and a few long contexts still use every SM. A unit cut
+// the 128-key tiles of the context. Items lie on one line, as long as they take
+// (kWeight), and CTA c of G takes [c W / G, (c + 1) W / G) of it, so any mix of
+// lengths is balanced and a few long contexts still use every SM. A unit cut
 // by CTA borders leaves (m, l, O) records; the last CTA to finish it merges them
 // (log-sum-exp). No CTA waits for another.
 //
@@ -47,6 +47,12 @@ constexpr int kMmaWarp = 8, kCopyWarp = 9;
 constexpr int kRows = 128;       // query rows of a half, keys of a tile
 constexpr int kTileBlocks = kRows / kBlockTokens;
 constexpr int kPart = kRows / 2; // keys of one softmax step
+// What an item takes, of a unit of two halves and of one: on bf16 pools 4700 and 3900
+// cycles a tile, each bound by its own chain of products and softmax (4 : 3 against
+// 1 : 1, the mixed batch 105.7 us against 112); on INT8/INT4 pools as much, the
+// conversion being the same (243 us against 254 with 4 : 3).
+constexpr int kWeight2 = 4;
+constexpr int weight_one(int kind) { return kind == 0 ? 3 : 4; }
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kConvWarps = 6;    // INT8/INT4: warps that turn codes into bf16
 constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
@@ -68,7 +74,8 @@ struct CrossParams {
     int64_t num_blocks;
     int32_t num_seqs;
     int32_t n_kv;
-    int32_t log2_g; // of the query heads per kv head
+    int32_t weight1; // of a one-half item (weight_one)
+    int32_t log2_g;  // of the query heads per kv head
     int32_t max_blocks;
     int32_t num_ctas;
     float scale_log2;
@@ -77,8 +84,13 @@ struct CrossParams {
 struct Seq {
     int32_t ctx, q0, nq;
     int32_t tiles;  // 128-key tiles
-    int32_t units;  // units of up to 256 packed query rows, of one kv head
-    __device__ int64_t items(int n_kv) const { return (int64_t)n_kv * tiles * units; }
+    int32_t pairs;  // units of one kv head's packed query rows with two halves,
+    int32_t units;  // and all of them (the last may have one)
+    __device__ int64_t head(const CrossParams &p) const // positions of one kv head
+    {
+        return (int64_t)tiles * (kWeight2 * (int64_t)pairs + p.weight1 * (units - pairs));
+    }
+    __device__ int64_t length(const CrossParams &p) const { return p.n_kv * head(p); }
 };
 
 // Sequence b's sizes; bad ones (reported where `report`) count as nothing.
@@ -95,7 +107,9 @@ __device__ __forceinline__ Seq load_seq(const CrossParams &p, int b, bool report
     s.q0 = q_ok ? q0 : 0;
     s.nq = q_ok ? q1 - q0 : 0;
     s.tiles = (int32_t)(((int64_t)s.ctx + kRows - 1) / kRows);
-    s.units = (int32_t)((((int64_t)s.nq << p.log2_g) + kUnitRows - 1) / kUnitRows);
+    const int64_t halves = (((int64_t)s.nq << p.log2_g) + kRows - 1) / kRows;
+    s.pairs = (int32_t)(halves / 2);
+    s.units = (int32_t)((halves + 1) / 2);
     return s;
 }
 
@@ -107,53 +121,53 @@ struct Segment {
     int rows;        // live rows: 1 .. 256
     int j0, j1;      // key tiles [j0, j1)
     int64_t first_v; // the unit's first position on the line
-    bool leading;    // starts at this CTA's first position
+    int weight;      // positions of one item
     bool whole;
 };
 
-// Where a CTA's range of the line starts.
+// The first item a CTA owns: an item belongs to the CTA with its first position.
 struct Start {
+    int64_t pos;
     int32_t b, kvh, qt, j; // sequence, kv head, unit of that head, key tile
 };
 
-// The segments of positions [lo, hi) of the line, one after another.
+// The segments of the items at positions [start, hi) of the line, one after another.
 struct Walk {
     const CrossParams &p;
-    int64_t pos, hi;
-    bool leading;
+    int64_t hi;
     Start at;
     Seq s;
 
-    __device__ Walk(const CrossParams &p_, int64_t lo, int64_t hi_, Start at_)
-        : p(p_), pos(lo), hi(hi_), leading(true), at(at_), s(load_seq(p_, at_.b, false))
+    __device__ Walk(const CrossParams &p_, int64_t hi_, const Start &at_)
+        : p(p_), hi(hi_), at(at_), s(load_seq(p_, at_.b, false))
     {
     }
 
     __device__ bool next(Segment &g)
     {
-        if (pos >= hi)
+        if (at.pos >= hi)
             return false;
-        if (!leading && at.qt == s.units) {
+        if (at.qt == s.units) {
             at.qt = 0;
             if (++at.kvh == p.n_kv) {
                 at.kvh = 0;
-                do // (pos is below the line's end, so there is a sequence with items)
+                do // (below the line's end there is a sequence with items)
                     s = load_seq(p, ++at.b, false);
                 while (s.tiles == 0 || s.units == 0);
             }
         }
-        const int n = (int)min((int64_t)(s.tiles - at.j), hi - pos);
+        g.halves = at.qt < s.pairs ? 2 : 1;
+        g.weight = g.halves == 2 ? kWeight2 : p.weight1;
+        const int64_t room = div_small(hi - at.pos + g.weight - 1, g.weight);
+        const int n = (int)min((int64_t)(s.tiles - at.j), room);
         g.kvh = at.kvh;
         g.j0 = at.j;
         g.j1 = at.j + n;
-        g.first_v = pos - at.j;
+        g.first_v = at.pos - (int64_t)at.j * g.weight;
         g.row0 = (int64_t)at.qt * kUnitRows;
         g.rows = (int)min((int64_t)kUnitRows, ((int64_t)s.nq << p.log2_g) - g.row0);
-        g.halves = g.rows > kRows ? 2 : 1;
-        g.whole = g.j0 == 0 && g.j1 == s.tiles;
-        g.leading = leading;
-        leading = false;
-        pos += n;
+        g.whole = n == s.tiles;
+        at.pos += (int64_t)n * g.weight;
         at.j = 0;
         ++at.qt;
         return true;
@@ -216,6 +230,12 @@ struct MergeState {
         }
     }
 };
+
+// CTAs that take part: each range is as long as the longest item, so that each owns one.
+__device__ __forceinline__ int64_t line_ctas(const CrossParams &p, int64_t total)
+{
+    return total == 0 ? 0 : max((int64_t)1, plan_ctas(p.num_ctas, total / kWeight2));
+}
 
 template <int D, int KIND>
 struct Smem {
@@ -373,7 +393,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                    p_full = s_full + 16 /* [half][part] */, o_full = p_full + 32,
                    a_full = o_full + 16, drained = a_full + 16, raw_full = drained + 8,
                    raw_empty = raw_full + 8 * L::RAWS;
-    // misc: [0] tensor memory base (0), [1] merge flag, [4..7] the range's start,
+    // misc: [0] tensor memory base (0), [1] merge flag, [2..7] the CTA's first item,
     // [8..] bad-block masks per slot, [16..17] per half, [18..23] blocks of
     // the tiles of codes, [24..] scan
     int32_t *misc = reinterpret_cast<int32_t *>(smem + L::kOffMisc);
@@ -393,7 +413,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         const int b0 = min(tid * per, p.num_seqs), b1 = min(b0 + per, p.num_seqs);
         int64_t sum = 0;
         for (int b = b0; b < b1; ++b)
-            sum += load_seq(p, b, blockIdx.x == 0).items(p.n_kv);
+            sum += load_seq(p, b, blockIdx.x == 0).length(p);
         int64_t x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -412,22 +432,25 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             total += wsum[w];
         }
         if (total > 0) {
-            const int64_t G = plan_ctas(p.num_ctas, total);
+            const int64_t G = line_ctas(p, total);
             const int64_t lo = plan_lo(blockIdx.x, total, G);
             if (blockIdx.x < G && lo >= before && lo < before + sum) {
                 int b = b0;
                 int64_t v = before;
-                for (;; ++b) { // the sequence that holds position lo (there is one)
-                    const int64_t c = load_seq(p, b, false).items(p.n_kv);
-                    if (lo < v + c)
-                        break;
-                    v += c;
+                Seq q = load_seq(p, b, false);
+                while (lo >= v + q.length(p)) { // (one of the thread's sequences holds lo)
+                    v += q.length(p);
+                    q = load_seq(p, ++b, false);
                 }
-                const Seq q = load_seq(p, b, false);
-                const int64_t head = (int64_t)q.tiles * q.units, in = lo - v;
-                const int64_t kvh = in / head, r = in - kvh * head, qt = r / q.tiles;
-                *reinterpret_cast<Start *>(misc + 4) = {b, (int32_t)kvh, (int32_t)qt,
-                                                        (int32_t)(r - qt * q.tiles)};
+                const int64_t head = q.head(p), kvh = (lo - v) / head, in = lo - v - kvh * head;
+                const int64_t pair = (int64_t)q.tiles * kWeight2;
+                const int64_t qt = min(in / pair, (int64_t)q.pairs);
+                const int64_t off = in - qt * pair, weight = qt < q.pairs ? kWeight2 : p.weight1;
+                const int64_t j = (off + weight - 1) / weight;
+                const bool past = j == q.tiles; // within the unit's last item: on to the next
+                *reinterpret_cast<Start *>(misc + 2) = {lo - off + j * weight, b, (int32_t)kvh,
+                                                        (int32_t)(past ? qt + 1 : qt),
+                                                        (int32_t)(past ? 0 : j)};
             }
         }
     }
@@ -441,10 +464,10 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    const int64_t G = plan_ctas(p.num_ctas, total);
+    const int64_t G = line_ctas(p, total);
     if (blockIdx.x >= G) // (no items: no CTA)
         return;
-    const int64_t lo = plan_lo(blockIdx.x, total, G), hi = plan_lo(blockIdx.x + 1, total, G);
+    const int64_t hi = plan_lo(blockIdx.x + 1, total, G);
 
     if (tid == 0) {
         mbar_init(q_full, 1);
@@ -473,7 +496,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = 0;
-    Walk walk(p, lo, hi, *reinterpret_cast<const Start *>(misc + 4));
+    Walk walk(p, hi, *reinterpret_cast<const Start *>(misc + 2));
     Segment g;
     bool dead = false; // a wait gave up: no more waits, no more copies or products
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -643,7 +666,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             __nv_bfloat16 *o_row =
                 p.out + ((walk.s.q0 + (prow >> p.log2_g)) * n_h + (g.kvh << p.log2_g) +
                          (prow & g_mask)) * D;
-            float *rec = record((int64_t)blockIdx.x * 2 + (g.leading ? 0 : 1));
+            float *rec = record((int64_t)blockIdx.x * 2 + (g.j0 > 0 ? 0 : 1));
             // 32 outputs from column c on, of a row whose weights sum to l
             auto emit = [&](int c, const float (&o)[32], float inv) {
                 if (live && g.whole) {
@@ -720,7 +743,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // ---- a cut unit: the last CTA to arrive merges its records
             bar_named(1, 2 * kRows);
             const int64_t c_first = plan_owner(g.first_v, total, G);
-            const int64_t last_v = g.first_v + walk.s.tiles - 1;
+            const int64_t last_v = g.first_v + (int64_t)(walk.s.tiles - 1) * g.weight;
             const int nseg = (int)(plan_owner(last_v, total, G) - c_first + 1);
             if (tid == 0) {
                 const int last = atomic_add_acq_rel_gpu(p.counters + c_first, 1) == nseg - 1;
@@ -731,10 +754,10 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             bar_named(1, 2 * kRows);
             if (!misc[1])
                 continue;
-            const int slot = g.first_v == plan_lo(c_first, total, G) ? 0 : 1;
+// (a CTA's records: 0 a unit it goes on with, 1 one that it begins)
             // thread: eight outputs of a row at a time, adjacent rows in adjacent threads; two
             // such pieces and up to two records are in flight together
-            const float *first = record(c_first * 2 + slot), *rest = record((c_first + 1) * 2);
+            const float *first = record(c_first * 2 + 1), *rest = record((c_first + 1) * 2);
             const int pieces = g.rows * (D / 8);
             for (int i0 = tid; i0 < pieces; i0 += 4 * kRows) {
                 MergeState st[2];
@@ -1124,6 +1147,7 @@ cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
     p.num_blocks = a.num_blocks;
     p.num_seqs = a.num_seqs;
     p.n_kv = a.n_kv;
+    p.weight1 = weight_one(a.kind);
     p.log2_g = a.g == 1 ? 0 : a.g == 2 ? 1 : a.g == 4 ? 2 : a.g == 8 ? 3 : 4;
     p.max_blocks = a.max_blocks;
     p.num_ctas = a.num_ctas;
