@@ -53,6 +53,11 @@ constexpr int kPart = kRows / 2; // keys of one softmax step
 // conversion being the same (243 us against 254 with 4 : 3).
 constexpr int kWeight2 = 4;
 constexpr int weight_one(int kind) { return kind == 0 ? 3 : 4; }
+// ... and each unit, in front of its first item, for its queries and outputs.
+#ifndef PA_CROSS_UNIT
+#define PA_CROSS_UNIT 5
+#endif
+constexpr int kUnitCost = PA_CROSS_UNIT;
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kConvWarps = 6;    // INT8/INT4: warps that turn codes into bf16
 constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
@@ -88,7 +93,9 @@ struct Seq {
     int32_t units;  // and all of them (the last may have one)
     __device__ int64_t head(const CrossParams &p) const // positions of one kv head
     {
-        return (int64_t)tiles * (kWeight2 * (int64_t)pairs + p.weight1 * (units - pairs));
+        return tiles == 0 ? 0
+                          : (int64_t)tiles * (kWeight2 * (int64_t)pairs + p.weight1 * (units - pairs)) +
+                                (int64_t)kUnitCost * units;
     }
     __device__ int64_t length(const CrossParams &p) const { return p.n_kv * head(p); }
 };
@@ -120,7 +127,7 @@ struct Segment {
     int64_t row0;    // first packed row of the unit within (sequence, kv head)
     int rows;        // live rows: 1 .. 256
     int j0, j1;      // key tiles [j0, j1)
-    int64_t first_v; // the unit's first position on the line
+    int64_t first_v; // the position of the unit's first item
     int weight;      // positions of one item
     bool whole;
 };
@@ -167,7 +174,7 @@ struct Walk {
         g.row0 = (int64_t)at.qt * kUnitRows;
         g.rows = (int)min((int64_t)kUnitRows, ((int64_t)s.nq << p.log2_g) - g.row0);
         g.whole = n == s.tiles;
-        at.pos += (int64_t)n * g.weight;
+        at.pos += (int64_t)n * g.weight + kUnitCost; // (to the next unit's first item)
         at.j = 0;
         ++at.qt;
         return true;
@@ -442,31 +449,39 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     v += q.length(p);
                     q = load_seq(p, ++b, false);
                 }
-                const int64_t head = q.head(p), kvh = (lo - v) / head, in = lo - v - kvh * head;
-                const int64_t pair = (int64_t)q.tiles * kWeight2;
-                const int64_t qt = min(in / pair, (int64_t)q.pairs);
-                const int64_t off = in - qt * pair, weight = qt < q.pairs ? kWeight2 : p.weight1;
-                const int64_t j = (off + weight - 1) / weight;
+                const int64_t head = q.head(p), kvh = div_small(lo - v, head);
+                const int64_t in = lo - v - kvh * head;
+                const int64_t pair = (int64_t)q.tiles * kWeight2 + kUnitCost;
+                const int64_t qt = min(div_small(in, pair), (int64_t)q.pairs);
+                const int64_t weight = qt < q.pairs ? kWeight2 : p.weight1;
+                // from the unit's first item on
+                const int64_t off = max(in - qt * pair - kUnitCost, (int64_t)0);
+                const int64_t j = div_small(off + weight - 1, weight);
                 const bool past = j == q.tiles; // within the unit's last item: on to the next
-                *reinterpret_cast<Start *>(misc + 2) = {lo - off + j * weight, b, (int32_t)kvh,
-                                                        (int32_t)(past ? qt + 1 : qt),
-                                                        (int32_t)(past ? 0 : j)};
+                const int64_t first_v = v + kvh * head + qt * pair + kUnitCost;
+                *reinterpret_cast<Start *>(misc + 2) = {
+                    first_v + j * weight + (past ? kUnitCost : 0), b, (int32_t)kvh,
+                    (int32_t)(past ? qt + 1 : qt), (int32_t)(past ? 0 : j)};
             }
         }
     }
-    // sequences without keys: zero rows
-    for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
-        const Seq s = load_seq(p, b, false);
-        if (s.nq > 0 && s.tiles == 0) {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)s.q0 * n_h * D);
-            const int64_t n = (int64_t)s.nq * n_h * (D / 8);
-            for (int64_t i = tid; i < n; i += kThreads)
-                dst[i] = make_uint4(0, 0, 0, 0);
+    // sequences without keys: zero rows (threads t of n)
+    auto zero_rows = [&](int t, int n) {
+        for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
+            const Seq q = load_seq(p, b, false);
+            if (q.nq > 0 && q.tiles == 0) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)q.q0 * n_h * D);
+                const int64_t chunks = (int64_t)q.nq * n_h * (D / 8);
+                for (int64_t i = t; i < chunks; i += n)
+                    dst[i] = make_uint4(0, 0, 0, 0);
+            }
         }
-    }
+    };
     const int64_t G = line_ctas(p, total);
-    if (blockIdx.x >= G) // (no items: no CTA)
+    if (blockIdx.x >= G) { // (no items: no CTA)
+        zero_rows(tid, kThreads);
         return;
+    }
     const int64_t hi = plan_lo(blockIdx.x + 1, total, G);
 
     if (tid == 0) {
@@ -1004,6 +1019,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     }
                 }
             }
+            zero_rows(lane, 32);
             if (dead) { // copies in flight land (bounded) before the memory goes
                 for (uint32_t n = n_kv > RING ? n_kv - RING : 0; n < n_kv; ++n)
                     mbar_poll(full0 + 8 * (n % RING), (n / RING) & 1u);
