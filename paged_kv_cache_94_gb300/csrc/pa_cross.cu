@@ -18,23 +18,31 @@
 // (log-sum-exp). No CTA waits for another.
 //
 // One CTA per SM, 12 warps (16 for INT8/INT4):
-//   warps 0-3, 4-7  softmax of half 0 and half 1, a thread per query row
-//   warp 8          issues the matrix instructions (one lane)
-//   warp 9          TMA copies of Q and of the paged K/V blocks (bf16: a block is 16
-//                   rows, 2 KiB boxes in the 128-byte swizzle)
+//   warps 0-3, 4-7  softmax of buffer 0 and buffer 1, a thread per query row
+//   warp 8          issues the matrix instructions (one thread)
+//   warp 9          copies of Q and of the paged K/V blocks: TMA boxes of 16 rows x 64
+//                   columns in the 128-byte swizzle; codes and scales as bulk copies
 //   warps 10-15     INT8/INT4 pools: write the codes that warp 9 copies as bf16
 //                   (exact: 8 significant bits) into the same tiles; the K
 //                   scale multiplies the scores, the V scale the weights
-// Tensor memory (512 columns): scores of both halves (128 fp32 columns each), their
-// outputs (d_h columns each). The weights P overwrite their half's
-// scores as bf16 and are the A operand of P V: one rounding of 2^-8 relative
-// per weight, of the size of the output's own; sums l take the unrounded
-// weights. While one half is in its softmax the other has the tensor cores. A
-// unit of one half uses both sets in turn, tile after tile, and joins its two
-// states at the end.
+// Tensor memory (512 columns): two buffers of scores (128 fp32 columns) and of outputs
+// (d_h columns). The weights P overwrite their scores as bf16 and are the A operand of
+// P V: one rounding of 2^-8 relative per weight, of the size of the output's own (the
+// error against 64 bits is 0.0023 where rounding the output alone costs 0.0017); sums l
+// take the unrounded weights. A unit of two halves gives each a buffer; one of one half
+// uses both in turn, tile after tile, and joins its two states at the end. So one
+// buffer is in its softmax while the other has the tensor cores.
 //
-// The softmax base of a row moves only when a tile's maximum exceeds it by more
+// The softmax base of a row moves only when a step's maximum exceeds it by more
 // than 2^8 (exact: P, l and O share one base), so O is rarely rescaled.
+//
+// Measured on a GB300 (g = 4, d_h 128, bf16): 8 prompts of 512..1024 tokens over
+// 4096..8192 keys 480 us, 1320 TFLOP/s, 0.68 of the measured bf16 matrix rate; a
+// buffer's chain (products 512 cycles, 290 until they are seen, scores 512, softmax
+// 1700) bounds a tile of 256 x 128 at 3350 cycles against 2048 of products. 48
+// sequences of 1..61 tokens over 200..4096 keys 106 us, 4200 GB/s, 0.63 of the
+// measured copy rate: 2700 cycles a tile, the K/V stream's own, and 30% of the time
+// in first loads, unit ends and merges.
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
 

@@ -13,14 +13,18 @@
 //   A row is 4 n bytes, read once: latency-bound. So a long row is cut over a
 //   cluster of up to 8 CTAs (counts joined in the first one's shared memory) and
 //   the keys stay in shared memory between the sweeps; rows too long for that
-//   read them again from L2.
+//   read them again from L2. 512 rows of 900..4096 tokens: 18 us a call, 32 of
+//   32K..128K: 31 us (11 and 40 thousand cycles a CTA: loads, then six steps of
+//   which each is one or two barriers).
 //
 // compact_kernel: row i of the new block table = row keep[i] of the old one,
 //   for K, V, their scales and the masses. Bound by HBM: each kept row is read
 //   and written once. A CTA moves 1024 16-byte pieces of K and as many of V:
 //   64 bf16 rows of 128, more of narrower ones. The rows' places are looked up
 //   once into shared memory; then every thread has eight 16-byte loads in
-//   flight before its first store.
+//   flight before its first store. 64 x 8 x 1024 bf16 rows of 128: 88.5 us, 6120
+//   GB/s, 0.91 of the measured copy rate; INT8 rows of 4 x 8 x 16384: 59.5 us, 0.71,
+//   each scattered scale costing a 32-byte sector.
 #include <cooperative_groups.h>
 
 #include "pa_internal.h"

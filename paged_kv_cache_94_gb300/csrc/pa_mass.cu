@@ -9,7 +9,8 @@
 // the scores costs 8 g bytes a token against the 4 d_h (bf16) of its K and V
 // rows; working them out a second time would read the K half again.
 //
-// HBM- or L2-bound. Each thread takes four adjacent tokens, so masses move as
+// HBM- or L2-bound: 9 us on top of the decode's 96 for 64 sequences of 512..4096 tokens
+// (bf16, 32 heads on 8), 14 on 122 for four of 32K..128K (INT8). Each thread takes four adjacent tokens, so masses move as
 // float4 whatever g is; units (b, kv head) are cut over blockIdx.y so that few
 // long contexts still fill the GPU.
 #include "pa_decode.cuh"
