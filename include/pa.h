@@ -397,6 +397,7 @@ size_t pa_cross_workspace_size(pa_geom geom, int32_t num_ctas);
  *   mass_out  the same shape (written): mass itself, to add in place, or
  *             another buffer, which leaves mass as it was. Entries j >= ctx_b
  *             are not written. Both 16-byte aligned.
+ * Where a row's softmax sum is not a number, so are its weights.
  * Weights are formed and added in fp32, in an order that does not depend on
  * how the work was split. A bad block's tokens have weight 0; a sequence with
  * a bad context length keeps its masses. Two sequences that share blocks have
@@ -430,7 +431,8 @@ size_t pa_decode_mass_workspace_size(pa_geom geom, int32_t num_seqs, int32_t max
  *   budget      > 0 tokens to keep; recent: 0 .. budget
  *   keep        int32 [num_seqs][n_kv][budget] (written): the kept tokens in
  *               ascending order, then -1
- *   keep_lens   int32 [num_seqs] (written): k
+ *   keep_lens   int32 [num_seqs] (written): k; not context_lens itself
+ *               (PA_ERR_SHAPE)
  *   dev_status  optional; a context length < 0 or > max_tokens sets
  *               PA_DEV_BAD_CONTEXT and keeps nothing of that sequence
  * num_seqs == 0 does nothing. The result is the same however it is computed.
@@ -454,8 +456,8 @@ pa_status pa_evict_select(const float *mass, int64_t max_tokens, const int32_t *
  *   new_tables    int32 [num_seqs][new_blocks_per_seq] (read): blocks that no
  *                 block table names, each once (pa_allocator_allocate_private
  *                 hands such blocks out); not block_tables itself
- *                 (PA_ERR_SHAPE). Sequences that share old blocks each get
- *                 their own copy. Slots behind a sequence's last row are left
+ *                 (PA_ERR_SHAPE); new_blocks_per_seq < 2^27. Sequences that
+ *                 share old blocks each get their own copy. Slots behind a sequence's last row are left
  *                 as they were.
  *   mass          fp32 [num_seqs][n_kv][max_blocks_per_seq * 16], mass_out fp32
  *                 [num_seqs][n_kv][new_blocks_per_seq * 16] (written; another

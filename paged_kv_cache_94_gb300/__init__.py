@@ -540,26 +540,28 @@ def _pool(k_cache, v_cache, k_scale, v_scale, n_h, device):
 
 
 _STREAM_WS: dict = {}
+_STREAM_LOCK = threading.RLock()  # held from taking a stream's workspace to the launch
 
 
 def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) -> torch.Tensor:
     """Workspace of one kind of call on the current stream, whose first `counters`
     bytes are zero (the calls leave them zero). Kept per stream, so calls on two streams do
     not share one. A prepared call (own) gets a buffer to itself, and a stream
-    that is being captured one of the graph's own, so those share none either."""
+    that is being captured one of the graph's own, so those share none either. The
+    caller holds _STREAM_LOCK until its call is issued: another thread's call on the
+    stream with fewer counters would write its scratch over this one's."""
     if own or torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws[:counters].zero_()
         return ws
     key = (kind, device.index, _stream_handle(device))
-    with _WS_LOCK:
-        ent = _STREAM_WS.get(key)
-        if ent is None or ent[0].numel() < nbytes:
-            ent = _STREAM_WS[key] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
-        if ent[1] < counters:
-            ent[0][:counters].zero_()
-        ent[1] = counters  # the rest is scratch
-        return ent[0]
+    ent = _STREAM_WS.get(key)
+    if ent is None or ent[0].numel() < nbytes:
+        ent = _STREAM_WS[key] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
+    if ent[1] < counters:
+        ent[0][:counters].zero_()
+    ent[1] = counters  # the rest is scratch
+    return ent[0]
 
 
 def _issue(fn, args, stream_index: int, what: str, result, device, stream, keep, prepare: bool):
@@ -612,7 +614,7 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             _take("mass", mass, torch.float32, dev),
             _take("mass_out", mass_out, torch.float32, dev), None, 0, g,
             _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
-    with _on(dev, stream):
+    with _on(dev, stream), _STREAM_LOCK:
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
@@ -663,7 +665,7 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
             _take("block_tables", block_tables, torch.int32, dev), mb,
             _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None, None, 0,
             g, _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
-    with _on(dev, stream):
+    with _on(dev, stream), _STREAM_LOCK:
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:

@@ -865,6 +865,9 @@ pa_status pa_evict_select(const float *mass, int64_t max_tokens, const int32_t *
     if (!aligned(mass, 4) || !aligned(context_lens, 4) || !aligned(keep, 4) ||
         !aligned(keep_lens, 4))
         return PA_ERR_ALIGNMENT;
+    // (written for one kv head while the others still read the context lengths)
+    if (keep_lens == context_lens)
+        return PA_ERR_SHAPE;
     int dev, sms;
     const pa_status st = current_device(dev, sms);
     if (st != PA_OK)
@@ -891,7 +894,8 @@ pa_status pa_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *
         new_blocks_per_seq <= 0)
         return PA_ERR_SHAPE;
     if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31) ||
-        (int64_t)num_seqs * new_blocks_per_seq >= (int64_t(1) << 31))
+        (int64_t)num_seqs * new_blocks_per_seq >= (int64_t(1) << 31) ||
+        new_blocks_per_seq > INT32_MAX / 16) // rows are counted in 32 bits
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0)
         return PA_OK;

@@ -62,10 +62,7 @@ constexpr int kPart = kRows / 2; // keys of one softmax step
 constexpr int kWeight2 = 4;
 constexpr int weight_one(int kind) { return kind == 0 ? 3 : 4; }
 // ... and each unit, in front of its first item, for its queries and outputs.
-#ifndef PA_CROSS_UNIT
-#define PA_CROSS_UNIT 5
-#endif
-constexpr int kUnitCost = PA_CROSS_UNIT;
+constexpr int kUnitCost = 5;
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kConvWarps = 6;    // INT8/INT4: warps that turn codes into bf16
 constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
@@ -777,7 +774,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             bar_named(1, 2 * kRows);
             if (!misc[1])
                 continue;
-// (a CTA's records: 0 a unit it goes on with, 1 one that it begins)
+            // (a CTA's records: 0 a unit it goes on with, 1 one that it begins)
             // thread: eight outputs of a row at a time, adjacent rows in adjacent threads; two
             // such pieces and up to two records are in flight together
             const float *first = record(c_first * 2 + 1), *rest = record((c_first + 1) * 2);

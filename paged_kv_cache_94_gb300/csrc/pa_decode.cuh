@@ -605,12 +605,13 @@ struct MergeRun {
     static_assert(GQ * D / RUN <= NT && D % RUN == 0, "one run per thread");
 };
 
-// Softmax base and reciprocal sum of query row h (MASS kernels).
+// Softmax base and reciprocal sum of query row h (MASS kernels): 0 without a
+// key, NaN when a score is not a number, as the row's weights then are.
 template <int GQ, int NQ>
 __device__ __forceinline__ void emit_ml(const DecodeParams &p, int b, int kvh, int h, float M,
                                         float L)
 {
-    p.ml[qo_row<GQ, NQ>(p, b, kvh, h)] = make_float2(M, L > 0.f ? 1.f / L : 0.f);
+    p.ml[qo_row<GQ, NQ>(p, b, kvh, h)] = make_float2(M, L != 0.f ? 1.f / L : 0.f);
 }
 
 template <int D, int GQ, int NW, int NQ, bool MASS = false>

@@ -97,13 +97,14 @@ select_kernel(const float *__restrict__ mass, int64_t stride,
     int32_t *out = keep + u * budget;
 
     // what needs no choice: the recent tokens, the unused tail, the count
-    for (int32_t i = want + rank * kSelThreads + tid; i < budget; i += C * kSelThreads)
-        out[i] = i < k ? m + (i - want) : -1;
+    // (64-bit indices: one step beyond a budget near 2^31 passes 32)
+    for (int64_t i = (int64_t)want + rank * kSelThreads + tid; i < budget; i += C * kSelThreads)
+        out[i] = i < k ? m + (int32_t)(i - want) : -1;
     if (tid == 0 && rank == 0 && u % n_kv == 0)
         keep_lens[b] = k;
     if (want == m) { // nothing to evict (the same in every CTA of the cluster)
-        for (int32_t i = rank * kSelThreads + tid; i < want; i += C * kSelThreads)
-            out[i] = i;
+        for (int64_t i = rank * kSelThreads + tid; i < want; i += C * kSelThreads)
+            out[i] = (int32_t)i;
         return;
     }
     if (want == 0)

@@ -84,6 +84,16 @@ def test_evict_compact_argument_checks(lib):
     assert call(mb=1 << 30) == -4
 
 
+def test_select_refuses_to_write_the_lengths_it_reads(lib):
+    assert lib.pa_evict_select(FAKE, 64, FAKE, 4, 8, 16, 4, OTHER, FAKE, None, None) == -2
+
+
+def test_compact_refuses_tables_of_more_rows_than_32_bits_count(lib):
+    """2^27 blocks of 16 rows for one sequence."""
+    assert lib.pa_evict_compact(FAKE, FAKE, None, None, FAKE, 16, FAKE, 16, FAKE, OTHER, 1 << 27, 1,
+                                FAKE, OTHER, _geom(), None, None) == -4
+
+
 def test_binding_refuses_cpu_tensors():
     q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
     kc = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)

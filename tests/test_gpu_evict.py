@@ -1,6 +1,7 @@
 """pa_decode_mass, pa_evict_select and pa_evict_compact on the GPU against their
 plain forms in 64 bits, apart and as one eviction step after another."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -113,6 +114,69 @@ def test_mass_matches_the_plain_form(kv, d, g, num_ctas):
             tol = wt * e + 2.0 ** -23 * want + 1e-37
             assert ((mass[b, h, :n].cpu().double() - want).abs() <= tol).all(), (b, h)
             assert torch.equal(mass[b, h, :n], other[b, h, :n])
+
+
+@pytest.mark.parametrize("num_ctas", [1, 40])
+@pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
+def test_mass_of_a_row_with_a_score_that_is_not_a_number(kv, num_ctas):
+    """One NaN among a kv head's scores makes all the weights of its rows NaN; the other kv
+    head's masses are untouched by it. Whole units (one CTA) and cut ones."""
+    gen = torch.Generator().manual_seed(12)
+    ctx, n_kv, g, d = [300, 1, 77], 2, 4, 128
+    bt, total, _ = make_tables(gen, ctx)
+    pool = make_pool(gen, total, n_kv, d, kv)
+    q = torch.randn(3, n_kv * g, d, generator=gen).to(torch.bfloat16).to(DEV)
+    cl = torch.tensor(ctx, dtype=torch.int32, device=DEV)
+    kw = dict(k_scale=pool[2], v_scale=pool[3], num_ctas=num_ctas)
+    clean = torch.zeros(3, n_kv, bt.shape[1] * 16, device=DEV)
+    pa.pa_decode_mass(q, pool[0], pool[1], bt.to(DEV), cl, 0.1, clean, **kw)
+    keys = pool[0] if kv == "bf16" else pool[2]      # a K row, or its scale
+    for b, j in ((0, 140), (1, 0)):
+        keys[int(bt[b, j // 16]), 1, j % 16] = float("nan")
+    mass = torch.zeros_like(clean)
+    pa.pa_decode_mass(q, pool[0], pool[1], bt.to(DEV), cl, 0.1, mass, **kw)
+    assert torch.isnan(mass[0, 1, :300]).all() and torch.isnan(mass[1, 1, :1]).all()
+    assert torch.equal(mass[:, 0], clean[:, 0]) and torch.equal(mass[2], clean[2])
+    assert (mass[0, 1, 300:] == 0).all() and (mass[1, 1, 1:] == 0).all()
+
+
+def test_two_threads_on_one_stream():
+    """Calls of different batch sizes share the stream's workspace, one after another."""
+    gen = torch.Generator().manual_seed(30)
+    n_kv, g, d = 8, 4, 128
+
+    def setting(B):
+        ctx = [1 + (37 * b) % 90 for b in range(B)]
+        bt, total, _ = make_tables(gen, ctx)
+        pool = make_pool(gen, total, n_kv, d, "bf16")
+        q = torch.randn(B, n_kv * g, d, generator=gen).to(torch.bfloat16).to(DEV)
+        args = (q, pool[0], pool[1], bt.to(DEV), torch.tensor(ctx, dtype=torch.int32, device=DEV))
+        mass = torch.zeros(B, n_kv, bt.shape[1] * 16, device=DEV)
+        want = torch.empty_like(mass)
+        out = pa.pa_decode_mass(*args, 0.1, mass, mass_out=want, num_ctas=64)
+        return args, mass, want, out
+
+    cases = [setting(200), setting(3)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(args, mass, want, out):
+        got = torch.empty_like(mass)
+        for _ in range(100):
+            o = pa.pa_decode_mass(*args, 0.1, mass, mass_out=got, num_ctas=64)
+        torch.cuda.synchronize()
+        for b, n in enumerate(args[4].tolist()):
+            if not torch.equal(got[b, :, :n], want[b, :, :n]):
+                wrong.append(b)
+        if not torch.equal(o, out):
+            wrong.append("out")
+
+    threads = [threading.Thread(target=run, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_mass_of_shared_blocks_bad_blocks_and_bad_lengths():
@@ -230,6 +294,17 @@ def test_select_matches_the_plain_choice(tokens, budget, recent):
     for b, n in enumerate(ctx):
         mass[b, :, n:] = float("nan")
     check_select(mass, ctx, budget, recent)
+
+
+def test_select_with_a_budget_near_2_31():
+    """The unused tail of one row is 8.6 GB long; its indices stay below 2^31."""
+    n, budget = 5000, 2 ** 31 - 1
+    keep, lens = pa.pa_evict_select(torch.rand(1, 1, n, device=DEV),
+                                    torch.tensor([n], dtype=torch.int32, device=DEV), budget, 3)
+    assert lens.tolist() == [n]
+    assert torch.equal(keep[0, 0, :n], torch.arange(n, dtype=torch.int32, device=DEV))
+    for part in keep[0, 0, n:].split(1 << 28):
+        assert int(part.min()) == int(part.max()) == -1
 
 
 @pytest.mark.parametrize("tokens,budget", [(20000, 900), (60001, 30000), (140003, 16384),
