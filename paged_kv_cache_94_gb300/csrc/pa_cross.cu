@@ -33,8 +33,7 @@
 // uses both in turn, tile after tile, and joins its two states at the end. So one
 // buffer is in its softmax while the other has the tensor cores.
 //
-// The softmax base of a row moves only when a step's maximum exceeds it by more
-// than 2^8 (exact: P, l and O share one base), so O is rarely rescaled.
+// The softmax base of a row moves rarely (kMoveLog2), so O is rarely rescaled.
 //
 // Measured on a GB300 (g = 4, d_h 128, bf16): 8 prompts of 512..1024 tokens over
 // 4096..8192 keys 480 us, 1320 TFLOP/s, 0.68 of the measured bf16 matrix rate; a
@@ -66,7 +65,11 @@ constexpr int kUnitCost = 5;
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kConvWarps = 6;    // INT8/INT4: warps that turn codes into bf16
 constexpr int kScaleRing = 8;    // tiles whose scales are kept (at most five live)
-constexpr float kMoveLog2 = 8.f; // see above
+// A row's softmax base moves only when a step's maximum exceeds it by more than this: exact,
+// since P, l and O share one base and weights up to 2^16 are as exact in bf16 as those up to 1
+// (the sums stay finite for |V| below 2^90). A move costs about 2000 cycles, the wait for the
+// products so far included: with 2^8 the INT8 batch took 242 us, with 2^16 221.
+constexpr float kMoveLog2 = 16.f;
 
 struct CrossParams {
     const void *k_cache;
@@ -385,6 +388,115 @@ __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity)
     return mbar_try_wait(bar, parity) || mbar_poll_slow(bar, parity);
 }
 
+// One step of the online softmax over 64 keys of an INT8/INT4 tile, of a warp's 32 rows. A
+// thread has four rows, lane / 4 + 8 i, and two of every eight keys: each scale that it loads
+// serves four rows: 16 loads of 8 bytes a step where a row per thread takes 32 of 16 (the INT8
+// batch in 213 us against 221).
+//   sk      K scales of the keys, V scales kRows behind
+//   here    keys of the step within the context; bad: its bad blocks, -1: no key is masked
+//   wait_o  O is complete
+template <int D, class WaitO>
+__device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float *sk, int c0,
+                                          int here, int bad, bool first, float (&m)[4],
+                                          float (&l)[4], WaitO wait_o)
+{
+    constexpr uint32_t kUpper = 16u << 16; // lanes 16 .. 31
+    const int lane = threadIdx.x & 31, c2 = 2 * (lane & 3);
+    float s[kPart]; // [i / 2][8 keys k][i % 2][2]
+    tmem_ld_quad(tS + c0, s);
+    tmem_ld_quad(tS + kUpper + c0, s + 32);
+    tmem_wait_ld();
+    tmem_landed<kPart>(s);
+    sk += c2;
+    auto at = [](int i, int k) { return (i / 2) * 32 + 4 * k + 2 * (i % 2); };
+#pragma unroll
+    for (int k = 0; k < 8; ++k) { // scores in the log2 domain
+        const float2 f = *reinterpret_cast<const float2 *>(sk + 8 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = mul2(make_float2(s[at(i, k)], s[at(i, k) + 1]), f);
+            s[at(i, k)] = x.x;
+            s[at(i, k) + 1] = x.y;
+        }
+    }
+    if (bad >= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool block = (bad >> (k / 2)) & 1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (block || 8 * k + c2 + e >= here)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[at(i, k) + e] = -INFINITY;
+        }
+    }
+    float top[4];
+    bool up = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        top[i] = fmaxf(s[at(i, 0)], s[at(i, 0) + 1]);
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+            top[i] = max3(top[i], s[at(i, k)], s[at(i, k) + 1]);
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        if (first)
+            m[i] = top[i];
+        up = up || top[i] > m[i] + kMoveLog2;
+    }
+    if (__any_sync(0xffffffffu, up)) {
+        wait_o();
+        float a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool move = top[i] > m[i] + kMoveLog2;
+            a[i] = move ? fast_exp2(m[i] - top[i]) : 1.f;
+            m[i] = move ? top[i] : m[i];
+            l[i] *= a[i];
+        }
+#pragma unroll 1
+        for (int c = 0; c < 2 * D; c += 64) { // columns c % D of the lower, then the upper lanes
+            const float a0 = c < D ? a[0] : a[2], a1 = c < D ? a[1] : a[3];
+            const uint32_t addr = tO + (c < D ? (uint32_t)c : kUpper + (uint32_t)(c - D));
+            float o[32];
+            tmem_ld_quad(addr, o);
+            tmem_wait_ld();
+            tmem_landed<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                o[e] *= e & 2 ? a1 : a0;
+            tmem_st_quad(addr, o);
+        }
+    }
+    float2 base[4], sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = m[i] == -INFINITY ? 0.f : -m[i];
+        base[i] = make_float2(x, x);
+        sum[i] = make_float2(0.f, 0.f);
+    }
+    uint32_t w[2][16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 f = *reinterpret_cast<const float2 *>(sk + kRows + 8 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 x = add2(make_float2(s[at(i, k)], s[at(i, k) + 1]), base[i]);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            sum[i] = add2(sum[i], x);
+            x = mul2(x, f);
+            w[i / 2][2 * k + i % 2] = pack_bf16x2(x.x, x.y);
+        }
+    }
+    tmem_st_quad_bf16(tS + c0 / 2, w[0]);
+    tmem_st_quad_bf16(tS + kUpper + c0 / 2, w[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        l[i] += sum[i].x + sum[i].y;
+}
+
 template <int D, int KIND>
 __global__ void __launch_bounds__(Smem<D, KIND>::kThreads, 1)
 cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -543,7 +655,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         uint32_t n_tile = 0;  // tiles of this CTA so far (the scale ring's index)
         while (walk.next(g)) {
             const int ctx = walk.s.ctx;
-            float m = -INFINITY, l = 0.f;
+            // this thread's row (INT8/INT4: its four rows, see there)
+            constexpr int kOwn = KIND ? 4 : 1;
+            float ms[kOwn], ls[kOwn];
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                ms[i] = -INFINITY;
+                ls[i] = 0.f;
+            }
             // two halves: each buffer one half, every tile; one half: both buffers its rows,
             // every other tile
             const bool two = g.halves == 2;
@@ -578,98 +697,93 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     const int c0 = part * kPart;
-                    float s[kPart];
-                    tmem_ld32(tS + c0, s);
-                    tmem_ld32(tS + c0 + 32, s + 32);
-                    tmem_wait_ld();
-                    tmem_landed<kPart>(s);
-                    // scores in the log2 domain = s * mul
-                    float mul = p.scale_log2;
+                    const bool first = part == 0 && j == j_first;
                     if constexpr (KIND != 0) {
-#pragma unroll
-                        for (int c = 0; c < kPart; c += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sk + c0 + c);
-                            const float2 a =
-                                mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
-                            const float2 b =
-                                mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
-                            s[c] = a.x;
-                            s[c + 1] = a.y;
-                            s[c + 2] = b.x;
-                            s[c + 3] = b.y;
-                        }
-                        mul = 1.f;
-                    }
-                    if (valid < kRows || bad || mul < 0.f) {
-                        const int here = valid - c0, bad_here = bad >> (c0 / kBlockTokens);
-#pragma unroll
-                        for (int c = 0; c < kPart; ++c)
-                            s[c] = c < here && !((bad_here >> (c / kBlockTokens)) & 1) ? s[c] * mul
-                                                                                       : -INFINITY;
-                        mul = 1.f;
-                    }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int c = 4; c < kPart - 4; c += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-                    const float *end = s + kPart - 4;
-                    const float top = mul * fmaxf(max3(mx[0], end[0], end[1]),
-                                                  fmaxf(max3(mx[1], end[2], end[3]),
-                                                        fmaxf(mx[2], mx[3])));
-                    if (part == 0 && j == j_first) {
-                        m = top;
+                        quad_step<D>(tS, tO, sk + c0, c0, valid - c0,
+                                     valid < kRows || bad ? bad >> (c0 / kBlockTokens) : -1, first,
+                                     ms, ls, [&]() {
+                                         if (part == 1) {
+                                             wait(a_full + 8 * half, n_s);
+                                             tc_fence_after();
+                                         }
+                                     });
                     } else {
-                        const bool up = top > m + kMoveLog2;
-                        if (__any_sync(0xffffffffu, up)) {
-                            // O holds every earlier tile, and in the second step the first's
-                            // products, once they are done
-                            if (part == 1) {
-                                wait(a_full + 8 * half, n_s);
-                                tc_fence_after();
-                            }
-                            const float a = up ? fast_exp2(m - top) : 1.f;
-                            m = up ? top : m;
-                            l *= a;
+                        float &m = ms[0], &l = ls[0];
+                        float s[kPart];
+                        tmem_ld32(tS + c0, s);
+                        tmem_ld32(tS + c0 + 32, s + 32);
+                        tmem_wait_ld();
+                        tmem_landed<kPart>(s);
+                        // scores in the log2 domain = s * mul
+                        float mul = p.scale_log2;
+                        if (valid < kRows || bad || mul < 0.f) {
+                            const int here = valid - c0, bad_here = bad >> (c0 / kBlockTokens);
+#pragma unroll
+                            for (int c = 0; c < kPart; ++c)
+                                s[c] = c < here && !((bad_here >> (c / kBlockTokens)) & 1)
+                                           ? s[c] * mul
+                                           : -INFINITY;
+                            mul = 1.f;
+                        }
+                        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int c = 4; c < kPart - 4; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+                        const float *end = s + kPart - 4;
+                        const float top = mul * fmaxf(max3(mx[0], end[0], end[1]),
+                                                      fmaxf(max3(mx[1], end[2], end[3]),
+                                                            fmaxf(mx[2], mx[3])));
+                        if (first) {
+                            m = top;
+                        } else {
+                            const bool up = top > m + kMoveLog2;
+                            if (__any_sync(0xffffffffu, up)) {
+                                // O holds every earlier tile, and in the second step the first's
+                                // products, once they are done
+                                if (part == 1) {
+                                    wait(a_full + 8 * half, n_s);
+                                    tc_fence_after();
+                                }
+                                const float a = up ? fast_exp2(m - top) : 1.f;
+                                m = up ? top : m;
+                                l *= a;
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                tmem_ld32(tO + c, o);
-                                tmem_wait_ld();
-                                tmem_landed<32>(o);
+                                for (int c = 0; c < D; c += 32) {
+                                    float o[32];
+                                    tmem_ld32(tO + c, o);
+                                    tmem_wait_ld();
+                                    tmem_landed<32>(o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] *= a;
-                                tmem_st32(tO + c, reinterpret_cast<const uint32_t *>(o));
+                                    for (int e = 0; e < 32; ++e)
+                                        o[e] *= a;
+                                    tmem_st32(tO + c, reinterpret_cast<const uint32_t *>(o));
+                                }
                             }
                         }
-                    }
-                    const float base = m == -INFINITY ? 0.f : m;
-                    const float2 mul_2 = make_float2(mul, mul), base_2 = make_float2(-base, -base);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t w[32];
+                        const float base = m == -INFINITY ? 0.f : m;
+                        const float2 mul_2 = make_float2(mul, mul);
+                        const float2 base_2 = make_float2(-base, -base);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < kPart; e += 4) {
-                        float2 x[2];
+                        for (int e = 0; e < kPart; e += 4) {
+                            float2 x[2];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int at = e + 2 * i;
-                            x[i] = fma2(make_float2(s[at], s[at + 1]), mul_2, base_2);
-                            x[i].x = fast_exp2(x[i].x);
-                            x[i].y = fast_exp2(x[i].y);
-                            sum[i] = add2(sum[i], x[i]);
+                            for (int i = 0; i < 2; ++i) {
+                                const int at = e + 2 * i;
+                                x[i] = fma2(make_float2(s[at], s[at + 1]), mul_2, base_2);
+                                x[i].x = fast_exp2(x[i].x);
+                                x[i].y = fast_exp2(x[i].y);
+                                sum[i] = add2(sum[i], x[i]);
+                            }
+                            w[e / 2] = pack_bf16x2(x[0].x, x[0].y);
+                            w[e / 2 + 1] = pack_bf16x2(x[1].x, x[1].y);
                         }
-                        if constexpr (KIND != 0) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sk + kRows + c0 + e);
-                            x[0] = mul2(x[0], make_float2(f.x, f.y));
-                            x[1] = mul2(x[1], make_float2(f.z, f.w));
-                        }
-                        w[e / 2] = pack_bf16x2(x[0].x, x[0].y);
-                        w[e / 2 + 1] = pack_bf16x2(x[1].x, x[1].y);
+                        tmem_st32(tS + c0 / 2, w);
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     }
-                    tmem_st32(tS + c0 / 2, w);
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(p_full + 16 * half + 8 * part);
@@ -705,7 +819,21 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
             };
             // (a sum that is not a number must not be skipped for its base)
-            m = l != l ? 0.f : m;
+            float m = ls[0] != ls[0] ? 0.f : ms[0], l = ls[0];
+            if constexpr (KIND != 0) { // from the quads to a row per thread
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) {
+                    float x = ls[i];
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    if ((lane & 3) == 0)
+                        states[half * kRows + (row & ~31) + 8 * i + lane / 4] =
+                            make_float2(x != x ? 0.f : ms[i], x);
+                }
+                __syncwarp();
+                m = states[half * kRows + row].x;
+                l = states[half * kRows + row].y;
+            }
             if (two) {
                 wait(o_full + 8 * half, n_s - 1);
                 tc_fence_after();
@@ -720,7 +848,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
             } else {
                 // both buffers' states of this row join; each thread takes half the columns
-                states[half * kRows + row] = make_float2(m, l);
+                if constexpr (KIND == 0)
+                    states[half * kRows + row] = make_float2(m, l);
                 bar_named(1, 2 * kRows);
                 const float2 s0 = states[row], s1 = states[kRows + row];
                 wait(o_full, n_b[0] - 1);
