@@ -45,8 +45,6 @@
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
 
-#include <type_traits>
-
 namespace pa {
 namespace {
 
@@ -54,12 +52,10 @@ constexpr int kMmaWarp = 8, kCopyWarp = 9;
 constexpr int kRows = 128;       // query rows of a half, keys of a tile
 constexpr int kTileBlocks = kRows / kBlockTokens;
 constexpr int kPart = kRows / 2; // keys of one softmax step
-// What an item takes, of a unit of two halves and of one: on bf16 pools 4700 and 3900
-// cycles a tile, each bound by its own chain of products and softmax (4 : 3 against
-// 1 : 1, the mixed batch 105.7 us against 112); on INT8/INT4 pools as much, the
-// conversion being the same (243 us against 254 with 4 : 3).
-constexpr int kWeight2 = 4;
-constexpr int weight_one(int kind) { return kind == 0 ? 3 : 4; }
+// What an item takes, of a unit of two halves and of one, in equal parts of about 1500 cycles:
+// on bf16 pools 4700 and 3900 cycles a tile (4 : 3 against 1 : 1: the mixed batch 105.7 us
+// against 112), on INT8 6000 and 4450 (199 us against 212).
+constexpr int kWeight2 = 4, kWeight1 = 3;
 // ... and each unit, in front of its first item, for its queries and outputs.
 constexpr int kUnitCost = 5;
 constexpr int kUnitRows = 2 * kRows;
@@ -87,7 +83,6 @@ struct CrossParams {
     int64_t num_blocks;
     int32_t num_seqs;
     int32_t n_kv;
-    int32_t weight1; // of a one-half item (weight_one)
     int32_t log2_g;  // of the query heads per kv head
     int32_t max_blocks;
     int32_t num_ctas;
@@ -99,13 +94,12 @@ struct Seq {
     int32_t tiles;  // 128-key tiles
     int32_t pairs;  // units of one kv head's packed query rows with two halves,
     int32_t units;  // and all of them (the last may have one)
-    __device__ int64_t head(const CrossParams &p) const // positions of one kv head
+    __device__ int64_t head() const // positions of one kv head
     {
-        return tiles == 0 ? 0
-                          : (int64_t)tiles * (kWeight2 * (int64_t)pairs + p.weight1 * (units - pairs)) +
-                                (int64_t)kUnitCost * units;
+        const int64_t items = kWeight2 * (int64_t)pairs + kWeight1 * (units - pairs);
+        return tiles == 0 ? 0 : tiles * items + (int64_t)kUnitCost * units;
     }
-    __device__ int64_t length(const CrossParams &p) const { return p.n_kv * head(p); }
+    __device__ int64_t length(const CrossParams &p) const { return p.n_kv * head(); }
 };
 
 // Sequence b's sizes; bad ones (reported where `report`) count as nothing.
@@ -172,7 +166,7 @@ struct Walk {
             }
         }
         g.halves = at.qt < s.pairs ? 2 : 1;
-        g.weight = g.halves == 2 ? kWeight2 : p.weight1;
+        g.weight = g.halves == 2 ? kWeight2 : kWeight1;
         const int64_t room = div_small(hi - at.pos + g.weight - 1, g.weight);
         const int n = (int)min((int64_t)(s.tiles - at.j), room);
         g.kvh = at.kvh;
@@ -566,11 +560,11 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     v += q.length(p);
                     q = load_seq(p, ++b, false);
                 }
-                const int64_t head = q.head(p), kvh = div_small(lo - v, head);
+                const int64_t head = q.head(), kvh = div_small(lo - v, head);
                 const int64_t in = lo - v - kvh * head;
                 const int64_t pair = (int64_t)q.tiles * kWeight2 + kUnitCost;
                 const int64_t qt = min(div_small(in, pair), (int64_t)q.pairs);
-                const int64_t weight = qt < q.pairs ? kWeight2 : p.weight1;
+                const int64_t weight = qt < q.pairs ? kWeight2 : kWeight1;
                 // from the unit's first item on
                 const int64_t off = max(in - qt * pair - kUnitCost, (int64_t)0);
                 const int64_t j = div_small(off + weight - 1, weight);
@@ -1202,40 +1196,34 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         }
                         // Chunk t + i * CONV of the tile: its row moves by STEP, a multiple of the
                         // swizzle's eight, so the addresses move by constants.
-                        auto convert = [&](auto checked) {
-                            uint32_t in = smem_u32(raw) + 16 * t, out = dst + t / CPR * 128;
+                        uint32_t in = smem_u32(raw) + 16 * t, out = dst + t / CPR * 128;
 #pragma unroll 1 // (unrolled, its instructions push the other warps' out of the cache)
-                            for (int r = t / CPR; r < kRows; r += STEP) {
-                                uint32_t w[4];
-                                lds128(in, w);
-                                // rows that are not there are zero (INT4: 8 is code 0)
-                                if (checked && !present(r))
-                                    w[0] = w[1] = w[2] = w[3] = 0;
-                                if constexpr (KIND == 1) {
-                                    // (a row's second 64 columns take its chunks in the other
-                                    // order: a row's eight threads then write to different banks)
-                                    const uint32_t a0 = flip ? w[2] : w[0], a1 = flip ? w[3] : w[1];
-                                    const uint32_t b0 = flip ? w[0] : w[2], b1 = flip ? w[1] : w[3];
-                                    sts128(out + at[0], code8_bf2<0x4140>(a0), code8_bf2<0x4342>(a0),
-                                           code8_bf2<0x4140>(a1), code8_bf2<0x4342>(a1));
-                                    sts128(out + at[1], code8_bf2<0x4140>(b0), code8_bf2<0x4342>(b0),
-                                           code8_bf2<0x4140>(b1), code8_bf2<0x4342>(b1));
-                                } else {
+                        for (int r = t / CPR; r < kRows; r += STEP) {
+                            uint32_t w[4];
+                            lds128(in, w);
+                            // rows that are not there are zero (INT4: 8 is code 0)
+                            if (!present(r))
+                                w[0] = w[1] = w[2] = w[3] = 0;
+                            if constexpr (KIND == 1) {
+                                // (a row's second 64 columns take its chunks in the other
+                                // order: a row's eight threads then write to different banks)
+                                const uint32_t a0 = flip ? w[2] : w[0], a1 = flip ? w[3] : w[1];
+                                const uint32_t b0 = flip ? w[0] : w[2], b1 = flip ? w[1] : w[3];
+                                sts128(out + at[0], code8_bf2<0x4140>(a0), code8_bf2<0x4342>(a0),
+                                       code8_bf2<0x4140>(a1), code8_bf2<0x4342>(a1));
+                                sts128(out + at[1], code8_bf2<0x4140>(b0), code8_bf2<0x4342>(b0),
+                                       code8_bf2<0x4140>(b1), code8_bf2<0x4342>(b1));
+                            } else {
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
-                                        sts128(out + at[i], code4_bf2<0>(a, b), code4_bf2<1>(a, b),
-                                               code4_bf2<2>(a, b), code4_bf2<3>(a, b));
-                                    }
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t a = w[i] ^ 0x88888888u, b = a >> 4;
+                                    sts128(out + at[i], code4_bf2<0>(a, b), code4_bf2<1>(a, b),
+                                           code4_bf2<2>(a, b), code4_bf2<3>(a, b));
                                 }
-                                in += 16 * CONV;
-                                out += STEP * 128;
                             }
-                        };
-                        if (valid == kRows && (mask & 0xff) == 0xff)
-                            convert(std::false_type());
-                        else
-                            convert(std::true_type());
+                            in += 16 * CONV;
+                            out += STEP * 128;
+                        }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -1297,7 +1285,6 @@ cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
     p.num_blocks = a.num_blocks;
     p.num_seqs = a.num_seqs;
     p.n_kv = a.n_kv;
-    p.weight1 = weight_one(a.kind);
     p.log2_g = a.g == 1 ? 0 : a.g == 2 ? 1 : a.g == 4 ? 2 : a.g == 8 ? 3 : 4;
     p.max_blocks = a.max_blocks;
     p.num_ctas = a.num_ctas;
