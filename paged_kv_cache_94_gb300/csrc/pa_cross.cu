@@ -36,7 +36,7 @@
 // The softmax base of a row moves rarely (kMoveLog2), so O is rarely rescaled.
 //
 // Measured on a GB300 (g = 4, d_h 128, bf16): 8 prompts of 512..1024 tokens over
-// 4096..8192 keys 480 us, 1320 TFLOP/s, 0.68 of the measured bf16 matrix rate; a
+// 4096..8192 keys 463 us, 1370 TFLOP/s, 0.70 of the measured bf16 matrix rate; a
 // buffer's chain (products 512 cycles, 290 until they are seen, scores 512, softmax
 // 1700) bounds a tile of 256 x 128 at 3350 cycles against 2048 of products. 48
 // sequences of 1..61 tokens over 200..4096 keys 106 us, 4200 GB/s, 0.63 of the
@@ -636,8 +636,10 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 
     if (warp < kMmaWarp) {
         // ================================================================ softmax
-        if constexpr (KIND != 0) // 256 x 160 + 256 x 96 = the 512 x 128 of the launch
+        if constexpr (KIND != 0) { // 256 x 160 + 256 x 96 = the 512 x 128 of the launch
+            static_assert(kThreads == 512, "whole groups of four warps share registers");
             asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        }
         const int half = warp >> 2;
         const int row = tid & (kRows - 1);
         // (m, l) of each buffer's rows, where the two buffers share a half's rows
@@ -1188,7 +1190,8 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         if (t == 0)
                             slot_mask[slot] = mask >> 8;
                         if (kv == 0 && t < kRows) {
-                            const float *in = reinterpret_cast<const float *>(raw + kRows * L::ROWB);
+                            const float *in =
+                                reinterpret_cast<const float *>(raw + kRows * L::ROWB);
                             float *sc = reinterpret_cast<float *>(smem + L::kOffScales) +
                                         (n_tile % kScaleRing) * 2 * kRows;
                             sc[t] = present(t) ? in[t] * p.scale_log2 : 0.f;
