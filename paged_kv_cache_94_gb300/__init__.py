@@ -475,6 +475,7 @@ def pa_decode_mq(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 _NO_SWITCH = contextlib.nullcontext()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device, stream):
@@ -484,7 +485,7 @@ def _on(device, stream):
         if stream.device != device:
             raise ValueError("stream and tensors are on different devices")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         return torch.cuda.device(device)
     return _NO_SWITCH
 
@@ -498,10 +499,9 @@ def _stream_handle(device) -> int:
 def _take(name: str, t: torch.Tensor, dtype, device) -> int:
     """The device pointer of a checked argument: a contiguous CUDA tensor of that
     dtype on that device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or \
-            not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index or \
+            t.dtype is not dtype or not t.is_contiguous():
         _need_cuda(name, t, dtype)
-    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     return t.data_ptr()
 
@@ -543,8 +543,9 @@ _STREAM_WS: dict = {}
 _STREAM_LOCK = threading.RLock()  # held from taking a stream's workspace to the launch
 
 
-def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) -> torch.Tensor:
-    """Workspace of one kind of call on the current stream, whose first `counters`
+def _stream_workspace(kind: str, nbytes: int, counters: int, device, stream: int,
+                      own: bool) -> torch.Tensor:
+    """Workspace of one kind of call on the current stream (its handle), whose first `counters`
     bytes are zero (the calls leave them zero). Kept per stream, so calls on two streams do
     not share one. A prepared call (own) gets a buffer to itself, and a stream
     that is being captured one of the graph's own, so those share none either. The
@@ -554,7 +555,7 @@ def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) 
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws[:counters].zero_()
         return ws
-    key = (kind, device.index, _stream_handle(device))
+    key = (kind, device.index, stream)
     ent = _STREAM_WS.get(key)
     if ent is None or ent[0].numel() < nbytes:
         ent = _STREAM_WS[key] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
@@ -564,11 +565,12 @@ def _stream_workspace(kind: str, nbytes: int, counters: int, device, own: bool) 
     return ent[0]
 
 
-def _issue(fn, args, stream_index: int, what: str, result, device, stream, keep, prepare: bool):
-    """Run a marshalled call on the current stream, or hand it out prepared."""
+def _issue(fn, args, stream_index: int, what: str, result, handle: int, stream, keep,
+           prepare: bool):
+    """Run a marshalled call on the current stream (its handle), or hand it out prepared."""
     if prepare:
         return Prepared(fn, args, stream_index, what, result, stream, keep)
-    args[stream_index] = _stream_handle(device)
+    args[stream_index] = handle
     st = fn(*args)
     if st != 0:
         raise PAError(st, what)
@@ -615,6 +617,7 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             _take("mass_out", mass_out, torch.float32, dev), None, 0, g,
             _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
     with _on(dev, stream), _STREAM_LOCK:
+        handle = _stream_handle(dev)
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
@@ -625,11 +628,12 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                 if nbytes == 0 and B > 0:
                     raise PAError(-4, "pa_decode_mass_workspace_size")
                 _WS_SIZES[key] = nbytes
-            workspace = _stream_workspace("mass", nbytes, _counter_bytes(g, B), dev, prepare)
+            workspace = _stream_workspace("mass", nbytes, _counter_bytes(g, B), dev, handle,
+                                          prepare)
         args[10] = _take("out", out, torch.bfloat16, dev)
         args[13] = _take("workspace", workspace, workspace.dtype, dev)
         args[14] = workspace.numel() * workspace.element_size()
-        return _issue(_lib().pa_decode_mass, args, 17, "pa_decode_mass", out, dev, stream,
+        return _issue(_lib().pa_decode_mass, args, 17, "pa_decode_mass", out, handle, stream,
                       workspace, prepare)
 
 
@@ -666,6 +670,7 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
             _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None, None, 0,
             g, _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
     with _on(dev, stream), _STREAM_LOCK:
+        handle = _stream_handle(dev)
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
@@ -678,11 +683,11 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
                 _WS_SIZES[key] = nbytes
             # (one counter per CTA in front of 2 * 256 * (d + 2) floats per CTA)
             counters = (nbytes // (512 * (d + 2) * 4) * 4 + 255) // 256 * 256
-            workspace = _stream_workspace("cross", nbytes, counters, dev, prepare)
+            workspace = _stream_workspace("cross", nbytes, counters, dev, handle, prepare)
         args[12] = _take("out", out, torch.bfloat16, dev)
         args[13] = _take("workspace", workspace, workspace.dtype, dev)
         args[14] = workspace.numel() * workspace.element_size()
-        return _issue(_lib().pa_cross_attention, args, 17, "pa_cross_attention", out, dev, stream,
+        return _issue(_lib().pa_cross_attention, args, 17, "pa_cross_attention", out, handle, stream,
                       workspace, prepare)
 
 
@@ -716,8 +721,8 @@ def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int,
         args = [mass.data_ptr(), tokens, ctx, B, n_kv, budget, recent,
                 _take("keep", keep, torch.int32, dev),
                 _take("keep_lens", keep_lens, torch.int32, dev), status, None]
-        return _issue(_lib().pa_evict_select, args, 10, "pa_evict_select", (keep, keep_lens), dev,
-                      stream, None, prepare)
+        return _issue(_lib().pa_evict_select, args, 10, "pa_evict_select", (keep, keep_lens),
+                      _stream_handle(dev), stream, None, prepare)
 
 
 def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -756,8 +761,8 @@ def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
             _opt("mass", mass, torch.float32, dev), _opt("mass_out", mass_out, torch.float32, dev),
             g, _opt("dev_status", dev_status, torch.int32, dev), None]
     with _on(dev, stream):
-        return _issue(_lib().pa_evict_compact, args, 16, "pa_evict_compact", None, dev, stream,
-                      None, prepare)
+        return _issue(_lib().pa_evict_compact, args, 16, "pa_evict_compact", None,
+                      _stream_handle(dev), stream, None, prepare)
 
 
 def pa_sink_write(k: torch.Tensor, v: torch.Tensor, seq_rows: torch.Tensor,
