@@ -43,6 +43,7 @@
 // measured copy rate: 2700 cycles a tile, the K/V stream's own, and 30% of the time
 // in first loads, unit ends and merges.
 #include "pa_decode.cuh"
+#include "pa_launch.h"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
@@ -1251,8 +1252,9 @@ cudaError_t launch_of(const CUtensorMap &tq, const CUtensorMap &tk, const CUtens
 {
     constexpr int bytes = Smem<D, KIND>::kBytes;
     static_assert(bytes <= 232448 && bytes > 116 * 1024, "one CTA per SM");
-    const cudaError_t e = cudaFuncSetAttribute(
-        cross_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<bool> raised[kRaisedDevices]; // the opt-in to that much, once per device
+    const cudaError_t e =
+        raise_shared_memory(raised, reinterpret_cast<const void *>(cross_kernel<D, KIND>), bytes);
     if (e != cudaSuccess)
         return e;
     cross_kernel<D, KIND><<<p.num_ctas, Smem<D, KIND>::kThreads, bytes, stream>>>(tq, tk, tv, p);

@@ -28,6 +28,7 @@
 #include <cooperative_groups.h>
 
 #include "pa_internal.h"
+#include "pa_launch.h"
 
 namespace cg = cooperative_groups;
 
@@ -437,9 +438,10 @@ cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t
     if (cached)
         cfg.dynamicSmemBytes = (size_t)per_thread * kSelThreads * sizeof(uint32_t);
     if (cfg.dynamicSmemBytes > 16 * 1024) { // (with the static part, over the 48 KiB default at most)
+        static std::atomic<bool> raised[2][kRaisedDevices]; // per kernel that keeps its keys
         const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kKeys * kSelThreads * (int)sizeof(uint32_t));
+            raise_shared_memory(raised[C > 1], reinterpret_cast<const void *>(kernel),
+                                kKeys * kSelThreads * (int)sizeof(uint32_t));
         if (e != cudaSuccess)
             return e;
     }
