@@ -13,7 +13,7 @@
 //   A row is 4 n bytes, read once: latency-bound. So a long row is cut over a
 //   cluster of up to 8 CTAs (counts joined in the first one's shared memory) and
 //   the keys stay in shared memory between the sweeps; rows too long for that
-//   read them again from L2. 512 rows of 900..4096 tokens: 18 us a call, 32 of
+//   read them again from L2. 512 rows of 900..4096 tokens: 17 us a call, 32 of
 //   32K..128K: 31 us (11 and 40 thousand cycles a CTA: loads, then six steps of
 //   which each is one or two barriers).
 //
@@ -67,8 +67,10 @@ struct SelShared {
 };
 
 // CACHED: the keys stay in shared memory (each thread's own). CLUSTER: several CTAs per row.
+// Three CTAs per SM where a CTA has a row to itself (many rows: 16.9 us against 18.4 with two),
+// two in a cluster (few rows; with three its registers spill, 32.8 us against 31.4).
 template <bool CACHED, bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads, 2)
+__global__ void __launch_bounds__(kSelThreads, CLUSTER ? 2 : 3)
 select_kernel(const float *__restrict__ mass, int64_t stride,
               const int32_t *__restrict__ context_lens, int n_kv, int budget, int recent,
               int32_t *__restrict__ keep, int32_t *__restrict__ keep_lens, int32_t *dev_status)
