@@ -141,9 +141,10 @@ pa_status ctas_per_sm(const DecodeKernel *kd, size_t smem, int &n)
     return PA_OK;
 }
 
-// One wave of resident CTAs of a kernel for a batch size.
-pa_status resident_ctas(const DecodeKernel *kd, int num_seqs, int &grid)
+// One wave of resident CTAs for a batch size.
+pa_status default_ctas(const pa_geom &g, int num_seqs, int &grid, int nq = 1)
 {
+    const DecodeKernel *kd = kernel_for(g, nq);
     if (!kd)
         return PA_ERR_UNSUPPORTED;
     int dev, sms, per;
@@ -155,11 +156,6 @@ pa_status resident_ctas(const DecodeKernel *kd, int num_seqs, int &grid)
         return st;
     grid = sms * per;
     return PA_OK;
-}
-
-pa_status default_ctas(const pa_geom &g, int num_seqs, int &grid, int nq = 1)
-{
-    return resident_ctas(kernel_for(g, nq), num_seqs, grid);
 }
 
 size_t counters_bytes(int64_t units) { return (size_t)((units * 4 + 255) / 256 * 256); }
@@ -396,7 +392,10 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
     const size_t smem = kd->smem_bytes(num_seqs);
     if ((st = ctas_per_sm(kd, smem, per)) != PA_OK)
         return st;
+    // (with masses the plain decode's grid: the split, and with it the output, are its own)
     int grid = num_ctas > 0 ? num_ctas : sms * per;
+    if (ma && num_ctas <= 0 && (st = default_ctas(g, num_seqs, grid)) != PA_OK)
+        return st;
     const DecodeKernel *kp = share ? pa::find_prefix_kernel(g.kv_dtype, g.d_h, group_of(g)) : nullptr;
     if (share && !kp)
         return PA_ERR_UNSUPPORTED;
@@ -748,9 +747,9 @@ size_t pa_decode_mass_workspace_size(pa_geom geom, int32_t num_seqs, int32_t max
     if (check_geom(geom) != PA_OK || num_seqs < 0 || num_seqs > kMaxSeqs || num_ctas < 0 ||
         max_blocks_per_seq <= 0 || (int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31))
         return 0;
-    const DecodeKernel *kd = pa::find_mass_kernel(geom.kv_dtype, geom.d_h, group_of(geom));
     int grid = num_ctas;
-    if (!kd || (grid == 0 && resident_ctas(kd, num_seqs, grid) != PA_OK))
+    if (!pa::find_mass_kernel(geom.kv_dtype, geom.d_h, group_of(geom)) ||
+        (grid == 0 && default_ctas(geom, num_seqs, grid) != PA_OK))
         return 0;
     return mass_layout(geom, num_seqs, max_blocks_per_seq, grid).end;
 }

@@ -12,9 +12,11 @@ template <int G>
 struct PolOf<128, G> {
     using type = QuantMmaPolicy<8, 128, G, 4, 2, (G >= 16 ? 1 : 3), 2, 1, false>;
 };
+// Three resident CTAs per SM, as the plain decode's registers allow up to this g without being
+// told (the score stores take a few more: left alone, 170 to 175 against its 168).
 template <int G>
 struct PolOf<64, G> {
-    using type = QuantMmaPolicy<8, 64, G, 4, 4, 1, 2, 1, false>;
+    using type = QuantMmaPolicy<8, 64, G, 4, 4, (G > 4 ? 1 : 3), 2, 1, false>;
 };
 
 template <int D, int G>

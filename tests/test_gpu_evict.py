@@ -116,6 +116,25 @@ def test_mass_matches_the_plain_form(kv, d, g, num_ctas):
             assert torch.equal(mass[b, h, :n], other[b, h, :n])
 
 
+@pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
+def test_output_is_the_decode_s_bit_for_bit_over_long_contexts(kv, d, g):
+    """Both calls on their default grids, with more key blocks than either has warps: every
+    unit is cut, at the same places in both only if the grids are equal."""
+    gen = torch.Generator().manual_seed(40 + g)
+    ctx, n_kv = [30000, 4097, 9001], 2
+    bt, total, _ = make_tables(gen, ctx)
+    pool = make_pool(gen, total, n_kv, d, kv)
+    q = torch.randn(len(ctx), n_kv * g, d, generator=gen).to(torch.bfloat16).to(DEV)
+    args = (q, pool[0], pool[1], bt.to(DEV), torch.tensor(ctx, dtype=torch.int32, device=DEV),
+            0.1)
+    mass = torch.zeros(len(ctx), n_kv, bt.shape[1] * 16, device=DEV)
+    kw = dict(k_scale=pool[2], v_scale=pool[3])
+    out = pa.pa_decode_mass(*args, mass, **kw)
+    assert torch.equal(out, pa.pa_decode(*args, **kw))
+
+
 @pytest.mark.parametrize("num_ctas", [1, 40])
 @pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
 def test_mass_of_a_row_with_a_score_that_is_not_a_number(kv, num_ctas):
