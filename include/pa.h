@@ -369,7 +369,9 @@ size_t pa_decode_mq_workspace_size(pa_geom geom, int32_t num_seqs, int32_t n_q,
  *             behind a decreasing offset, get either one's result.
  *   num_ctas  0: one CTA per SM; 1 .. 8192: that many
  * Scores, softmax sums and outputs accumulate in fp32; a weight (times its V
- * scale) is rounded once to bf16, 2^-8 relative, before the products with V.
+ * scale) enters the products with V as two bf16 parts, 2^-16 relative. An
+ * infinite V entry gives infinity or NaN, as in pa_decode; sums are finite for
+ * |V| below 2^90.
  * Results do not depend on how the work was split beyond fp32 rounding, and are
  * the same from call to call. The pages have no counterpart: they attend a
  * request's own tokens.

@@ -26,12 +26,14 @@
 //                   (exact: 8 significant bits) into the same tiles; the K
 //                   scale multiplies the scores, the V scale the weights
 // Tensor memory (512 columns): two buffers of scores (128 fp32 columns) and of outputs
-// (d_h columns). The weights P overwrite their scores as bf16 and are the A operand of
-// P V: one rounding of 2^-8 relative per weight, of the size of the output's own (the
-// error against 64 bits is 0.0023 where rounding the output alone costs 0.0017); sums l
-// take the unrounded weights. A unit of two halves gives each a buffer; one of one half
-// uses both in turn, tile after tile, and joins its two states at the end. So one
-// buffer is in its softmax while the other has the tensor cores.
+// (d_h columns). The weights P overwrite their scores as two bf16 parts each, what rounding
+// leaves of the first in the second, and both are A operands of P V: 2^-16 relative per
+// weight. With the first part alone (2^-8) rows of V that span 1e-3 .. 1e3 and cancel leave
+// the decode's tolerance of 1e-2 (1 + |out|). It costs half as many products again and the
+// forming of the second parts: prompts 465 -> 617 us and up, mixed batch 105 -> 121, INT8
+// 198 -> 230. Sums l take the unrounded weights. A unit of two halves gives each a buffer;
+// one of one half uses both in turn, tile after tile, and joins its two states at the end.
+// So one buffer is in its softmax while the other has the tensor cores.
 //
 // The softmax base of a row moves rarely (kMoveLog2), so O is rarely rescaled.
 //
@@ -53,9 +55,8 @@ constexpr int kMmaWarp = 8, kCopyWarp = 9;
 constexpr int kRows = 128;       // query rows of a half, keys of a tile
 constexpr int kTileBlocks = kRows / kBlockTokens;
 constexpr int kPart = kRows / 2; // keys of one softmax step
-// What an item takes, of a unit of two halves and of one, in equal parts of about 1500 cycles:
-// on bf16 pools 4700 and 3900 cycles a tile (4 : 3 against 1 : 1: the mixed batch 105.7 us
-// against 112), on INT8 6000 and 4450 (199 us against 212).
+// What an item takes, of a unit of two halves and of one: 4 : 3 against 1 : 1 and 2 : 1 in us:
+// the mixed batch 121 / 130 / 135, INT8 230 / 242 / 267, heads of 64 103 / 110 / 97.
 constexpr int kWeight2 = 4, kWeight1 = 3;
 // ... and each unit, in front of its first item, for its queries and outputs.
 constexpr int kUnitCost = 5;
@@ -331,6 +332,16 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return *reinterpret_cast<float2 *>(&r);
 }
 
+// Two weights in two bf16 parts each: hi rounds them, lo rounds what is left of them (exact in
+// fp32), 2^-16 relative together.
+__device__ __forceinline__ void split_bf16x2(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 r = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                          make_float2(-1.f, -1.f), x);
+    lo = pack_bf16x2(r.x, r.y);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -471,7 +482,7 @@ __device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float 
         base[i] = make_float2(x, x);
         sum[i] = make_float2(0.f, 0.f);
     }
-    uint32_t w[2][16];
+    uint32_t w[2][16], low[2][16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float2 f = *reinterpret_cast<const float2 *>(sk + kRows + 8 * k);
@@ -481,12 +492,15 @@ __device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float 
             x.x = fast_exp2(x.x);
             x.y = fast_exp2(x.y);
             sum[i] = add2(sum[i], x);
-            x = mul2(x, f);
-            w[i / 2][2 * k + i % 2] = pack_bf16x2(x.x, x.y);
+            split_bf16x2(mul2(x, f), w[i / 2][2 * k + i % 2], low[i / 2][2 * k + i % 2]);
         }
     }
-    tmem_st_quad_bf16(tS + c0 / 2, w[0]);
-    tmem_st_quad_bf16(tS + kUpper + c0 / 2, w[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t at_lanes = tS + (i ? kUpper : 0u) + c0;
+        tmem_st_quad_bf16(at_lanes, w[i]);
+        tmem_st_quad_bf16(at_lanes + kPart / 2, low[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         l[i] += sum[i].x + sum[i].y;
@@ -763,7 +777,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         const float2 mul_2 = make_float2(mul, mul);
                         const float2 base_2 = make_float2(-base, -base);
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        uint32_t w[32];
+                        uint32_t w[32], low[32];
 #pragma unroll
                         for (int e = 0; e < kPart; e += 4) {
                             float2 x[2];
@@ -775,10 +789,11 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                 x[i].y = fast_exp2(x[i].y);
                                 sum[i] = add2(sum[i], x[i]);
                             }
-                            w[e / 2] = pack_bf16x2(x[0].x, x[0].y);
-                            w[e / 2 + 1] = pack_bf16x2(x[1].x, x[1].y);
+                            split_bf16x2(x[0], w[e / 2], low[e / 2]);
+                            split_bf16x2(x[1], w[e / 2 + 1], low[e / 2 + 1]);
                         }
-                        tmem_st32(tS + c0 / 2, w);
+                        tmem_st32(tS + c0, w);
+                        tmem_st32(tS + c0 + kPart / 2, low);
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     }
                     tmem_wait_st();
@@ -977,6 +992,15 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     }
                     return ready(kv_full + 8 * at, parity);
                 };
+                // output (+)= P V over 64 keys: both parts of the weights with one V tile
+                auto products = [&](uint32_t tO, uint32_t tP, uint64_t v_desc, uint32_t more) {
+#pragma unroll
+                    for (int kk = 0; kk < kPart / 16; ++kk) {
+                        tc_mma_ts(tO, tP + 8 * kk, v_desc + kk * (2048 >> 4), iO,
+                                  kk > 0 ? 1 : more);
+                        tc_mma_ts(tO, tP + kPart / 2 + 8 * kk, v_desc + kk * (2048 >> 4), iO, 1);
+                    }
+                };
                 while (walk.next(g)) {
                     const int n = g.j1 - g.j0;
                     const bool two = g.halves == 2;
@@ -1003,17 +1027,12 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                             if (!ready(p_full + 16 * b, np >> b))
                                 break;
                             tc_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < kRows / 32; ++kk)
-                                tc_mma_ts(tO, tS + 8 * kk, v_desc + kk * (2048 >> 4), iO,
-                                          kk > 0 ? 1 : more);
+                            products(tO, tS, v_desc, more);
                             tc_commit(a_full + 8 * b);
                             if (!ready(p_full + 16 * b + 8, np >> b))
                                 break;
                             tc_fence_after();
-#pragma unroll
-                            for (int kk = kRows / 32; kk < kRows / 16; ++kk)
-                                tc_mma_ts(tO, tS + 8 * kk, v_desc + kk * (2048 >> 4), iO, 1);
+                            products(tO, tS + kPart, v_desc + (kPart / 16) * (2048 >> 4), 1);
                             tc_commit(o_full + 8 * b);
                             if (give)
                                 tc_commit(kv_empty + 8 * vs);
