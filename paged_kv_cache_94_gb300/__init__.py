@@ -215,14 +215,16 @@ class Prepared:
     by calling it: for a serving loop that repeats the same call on the same
     buffers (the tensors' contents may change, not their addresses or shapes).
     The stream is the one given at preparation, else the current stream at
-    each call. Returns what the unprepared call returns (the output tensor)."""
+    each call. Returns what the unprepared call returns (the output tensor).
+    A prepared call has one workspace: its calls, and replays of graphs that
+    captured it, are ordered one after another, and it is kept as long as such
+    a graph."""
 
-    __slots__ = ("_fn", "_args", "_si", "_what", "_result", "_stream", "_keep")
+    __slots__ = ("_fn", "_args", "_si", "_what", "_result", "_stream")
 
-    def __init__(self, fn, args, stream_index, what, result, stream, keep=None):
+    def __init__(self, fn, args, stream_index, what, result, stream):
         self._fn, self._args, self._si = fn, list(args), stream_index
         self._what, self._result, self._stream = what, result, stream
-        self._keep = keep  # what lives as long as the call (its workspace)
 
     def __call__(self):
         self._args[self._si] = _stream_ptr(self._stream)
@@ -543,15 +545,14 @@ _STREAM_WS: dict = {}
 _STREAM_LOCK = threading.RLock()  # held from taking a stream's workspace to the launch
 
 
-def _stream_workspace(kind: str, nbytes: int, counters: int, device, stream: int,
-                      own: bool) -> torch.Tensor:
+def _stream_workspace(kind: str, nbytes: int, counters: int, device, stream: int) -> torch.Tensor:
     """Workspace of one kind of call on the current stream (its handle), whose first `counters`
     bytes are zero (the calls leave them zero). Kept per stream, so calls on two streams do
-    not share one. A prepared call (own) gets a buffer to itself, and a stream
-    that is being captured one of the graph's own, so those share none either. The
-    caller holds _STREAM_LOCK until its call is issued: another thread's call on the
-    stream with fewer counters would write its scratch over this one's."""
-    if own or torch.cuda.is_current_stream_capturing():
+    not share one. A stream that is being captured gets one of the graph's own, so graphs
+    share none either (nor does a prepared call: _Owned). The caller holds _STREAM_LOCK
+    until its call is issued: another thread's call on the stream with fewer counters
+    would write its scratch over this one's."""
+    if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws[:counters].zero_()
         return ws
@@ -565,11 +566,81 @@ def _stream_workspace(kind: str, nbytes: int, counters: int, device, stream: int
     return ent[0]
 
 
-def _issue(fn, args, stream_index: int, what: str, result, handle: int, stream, keep,
-           prepare: bool):
-    """Run a marshalled call on the current stream (its handle), or hand it out prepared."""
-    if prepare:
-        return Prepared(fn, args, stream_index, what, result, stream, keep)
+_SIDE_STREAMS: dict = {}
+
+
+class _Owned:
+    """What a prepared call allocates for itself: results and a workspace, good on
+    whatever stream issues the call. They come from a stream of the library's own that has
+    run dry before the call is handed out, so no earlier work still uses them and the
+    workspace's counters are zero; each stream that issues the call is recorded, so they
+    are not handed out again under it. A call prepared while its stream is captured takes
+    them from the graph and zeroes its counters at every call, since what the capture
+    holds has not run yet."""
+
+    __slots__ = ("_device", "_side", "_tensors", "_zero", "_streams")
+
+    def __init__(self, device):
+        self._device, self._side = device, None
+        self._tensors, self._zero, self._streams = [], None, set()
+        if not torch.cuda.is_current_stream_capturing():
+            self._side = _SIDE_STREAMS.get(device.index)
+            if self._side is None:
+                self._side = _SIDE_STREAMS[device.index] = torch.cuda.Stream(device, priority=-1)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        with torch.cuda.stream(self._side):  # (None: no switch)
+            t = torch.empty(shape, dtype=dtype, device=self._device)
+        if self._side is not None:
+            self._side.synchronize()
+        self._tensors.append(t)
+        return t
+
+    def workspace(self, nbytes: int, counters: int) -> torch.Tensor:
+        ws = self.empty(nbytes, torch.uint8)
+        if self._side is None:
+            self._zero = ws[:counters]
+        else:
+            with torch.cuda.stream(self._side):
+                ws[:counters].zero_()
+            self._side.synchronize()
+        return ws
+
+    def issued_on(self, handle: int):
+        """The current stream (its handle) is about to run the call."""
+        if handle not in self._streams:
+            self._streams.add(handle)
+            for t in self._tensors:
+                t.record_stream(torch.cuda.current_stream(self._device))
+        if self._zero is not None:
+            self._zero.zero_()
+
+
+class _PreparedOwner(Prepared):
+    """A prepared call with the memory that it allocated."""
+
+    __slots__ = ("_device", "_owned")
+
+    def __init__(self, fn, args, stream_index, what, result, stream, device, owned):
+        super().__init__(fn, args, stream_index, what, result, stream)
+        self._device, self._owned = device, owned
+
+    def __call__(self):
+        with _on(self._device, self._stream):
+            handle = self._args[self._si] = _stream_handle(self._device)
+            self._owned.issued_on(handle)
+            st = self._fn(*self._args)
+        if st != 0:
+            raise PAError(st, self._what)
+        return self._result
+
+
+def _issue(fn, args, stream_index: int, what: str, result, handle: int, stream, device,
+           owned: Optional[_Owned]):
+    """Run a marshalled call on the current stream (its handle), or (owned) hand it out
+    prepared."""
+    if owned is not None:
+        return _PreparedOwner(fn, args, stream_index, what, result, stream, device, owned)
     args[stream_index] = handle
     st = fn(*args)
     if st != 0:
@@ -618,8 +689,9 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
     with _on(dev, stream), _STREAM_LOCK:
         handle = _stream_handle(dev)
+        owned = _Owned(dev) if prepare else None
         if out is None:
-            out = torch.empty_like(q)
+            out = owned.empty(q.shape, q.dtype) if prepare else torch.empty_like(q)
         if workspace is None:
             key = ("mass", dev.index, g.num_blocks, n_h, g.n_kv, d, g.kv_dtype, B, mb, num_ctas)
             nbytes = _WS_SIZES.get(key)
@@ -628,13 +700,14 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                 if nbytes == 0 and B > 0:
                     raise PAError(-4, "pa_decode_mass_workspace_size")
                 _WS_SIZES[key] = nbytes
-            workspace = _stream_workspace("mass", nbytes, _counter_bytes(g, B), dev, handle,
-                                          prepare)
+            counters = _counter_bytes(g, B)
+            workspace = (owned.workspace(nbytes, counters) if prepare else
+                         _stream_workspace("mass", nbytes, counters, dev, handle))
         args[10] = _take("out", out, torch.bfloat16, dev)
         args[13] = _take("workspace", workspace, workspace.dtype, dev)
         args[14] = workspace.numel() * workspace.element_size()
-        return _issue(_lib().pa_decode_mass, args, 17, "pa_decode_mass", out, handle, stream,
-                      workspace, prepare)
+        return _issue(_lib().pa_decode_mass, args, 17, "pa_decode_mass", out, handle, stream, dev,
+                      owned)
 
 
 def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tensor,
@@ -671,8 +744,9 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
             g, _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
     with _on(dev, stream), _STREAM_LOCK:
         handle = _stream_handle(dev)
+        owned = _Owned(dev) if prepare else None
         if out is None:
-            out = torch.empty_like(q)
+            out = owned.empty(q.shape, q.dtype) if prepare else torch.empty_like(q)
         if workspace is None:
             key = ("cross", dev.index, d, num_ctas)
             nbytes = _WS_SIZES.get(key)
@@ -683,12 +757,13 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
                 _WS_SIZES[key] = nbytes
             # (one counter per CTA in front of 2 * 256 * (d + 2) floats per CTA)
             counters = (nbytes // (512 * (d + 2) * 4) * 4 + 255) // 256 * 256
-            workspace = _stream_workspace("cross", nbytes, counters, dev, handle, prepare)
+            workspace = (owned.workspace(nbytes, counters) if prepare else
+                         _stream_workspace("cross", nbytes, counters, dev, handle))
         args[12] = _take("out", out, torch.bfloat16, dev)
         args[13] = _take("workspace", workspace, workspace.dtype, dev)
         args[14] = workspace.numel() * workspace.element_size()
         return _issue(_lib().pa_cross_attention, args, 17, "pa_cross_attention", out, handle, stream,
-                      workspace, prepare)
+                      dev, owned)
 
 
 def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int, recent: int = 0,
@@ -714,15 +789,18 @@ def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int,
     ctx = _take("context_lens", context_lens, torch.int32, dev)
     status = _opt("dev_status", dev_status, torch.int32, dev)
     with _on(dev, stream):
+        owned = _Owned(dev) if prepare else None
         if keep is None:
-            keep = torch.empty((B, n_kv, budget), dtype=torch.int32, device=dev)
+            keep = (owned.empty((B, n_kv, budget), torch.int32) if prepare else
+                    torch.empty((B, n_kv, budget), dtype=torch.int32, device=dev))
         if keep_lens is None:
-            keep_lens = torch.empty(B, dtype=torch.int32, device=dev)
+            keep_lens = (owned.empty(B, torch.int32) if prepare else
+                         torch.empty(B, dtype=torch.int32, device=dev))
         args = [mass.data_ptr(), tokens, ctx, B, n_kv, budget, recent,
                 _take("keep", keep, torch.int32, dev),
                 _take("keep_lens", keep_lens, torch.int32, dev), status, None]
         return _issue(_lib().pa_evict_select, args, 10, "pa_evict_select", (keep, keep_lens),
-                      _stream_handle(dev), stream, None, prepare)
+                      _stream_handle(dev), stream, dev, owned)
 
 
 def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -762,7 +840,7 @@ def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
             g, _opt("dev_status", dev_status, torch.int32, dev), None]
     with _on(dev, stream):
         return _issue(_lib().pa_evict_compact, args, 16, "pa_evict_compact", None,
-                      _stream_handle(dev), stream, None, prepare)
+                      _stream_handle(dev), stream, dev, _Owned(dev) if prepare else None)
 
 
 def pa_sink_write(k: torch.Tensor, v: torch.Tensor, seq_rows: torch.Tensor,
