@@ -559,6 +559,8 @@ def _stream_workspace(kind: str, nbytes: int, counters: int, device, stream: int
     key = (kind, device.index, stream)
     ent = _STREAM_WS.get(key)
     if ent is None or ent[0].numel() < nbytes:
+        ent = None  # the smaller one goes first (its last use is earlier on this stream)
+        _STREAM_WS.pop(key, None)
         ent = _STREAM_WS[key] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
     if ent[1] < counters:
         ent[0][:counters].zero_()
@@ -662,7 +664,14 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     mass: float32 [B, n_kv, max_blocks * 16], entry j for the token at
     block_tables[b][j // 16], offset j % 16; the sums go to mass_out (default: in
     place). Entries at and behind a context's end are not written. Everything
-    else, and the result, as pa_decode."""
+    else, and the result, as pa_decode.
+
+    The workspace holds a score per query head and block-table slot, 4 * B * n_h *
+    max_blocks * 16 bytes (64 sequences, 32 heads, a table of 128K tokens: 1.07 GB),
+    and pa_decode's counters and records. The one that the library allocates is kept for
+    the stream until a call needs a larger one; workspace (uint8, at least
+    pa_decode_mass_workspace_size bytes, its counters zero as pa_decode's) is the
+    caller's own."""
     _need_cuda("q", q, torch.bfloat16)
     dev = q.device
     if q.dim() != 3 or block_tables.dim() != 2:

@@ -198,6 +198,33 @@ def test_two_threads_on_one_stream():
     assert not wrong
 
 
+def test_a_stream_s_larger_workspace_replaces_the_smaller_one():
+    """A wider table needs a larger workspace: both are never held at once."""
+    gen = torch.Generator().manual_seed(50)
+    ctx, n_kv, g, d = [100] * 8, 4, 4, 64
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        args = []
+        for extra in (1000, 2000):
+            bt, total, _ = make_tables(gen, ctx, extra=extra)
+            pool = make_pool(gen, total, n_kv, d, "bf16")
+            q = torch.randn(8, n_kv * g, d, generator=gen).to(torch.bfloat16).to(DEV)
+            args.append((q, pool[0], pool[1], bt.to(DEV),
+                         torch.tensor(ctx, dtype=torch.int32, device=DEV), 0.1,
+                         torch.zeros(8, n_kv, bt.shape[1] * 16, device=DEV)))
+        out = [torch.empty_like(a[0]) for a in args]
+        pa.pa_decode_mass(*args[0], out=out[0])
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        pa.pa_decode_mass(*args[1], out=out[1])
+        torch.cuda.synchronize()
+        larger = 4 * 8 * n_kv * g * (2000 + 7) * 16
+        assert torch.cuda.max_memory_allocated() - before < larger
+        assert torch.cuda.memory_allocated() - before > larger // 4
+
+
 def test_mass_of_shared_blocks_bad_blocks_and_bad_lengths():
     gen = torch.Generator().manual_seed(3)
     ctx = [40, 40, 100, 64, 30]
