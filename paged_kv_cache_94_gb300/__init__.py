@@ -475,6 +475,14 @@ def pa_decode_mq(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return call if prepare else call()
 
 
+def _int32(name: str, x) -> int:
+    """x as the C ABI's int32 (a larger number would be cut to its low bits on the way)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 _NO_SWITCH = contextlib.nullcontext()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -689,7 +697,7 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         _need_cuda("out", out, torch.bfloat16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-    num_ctas = int(num_ctas)
+    num_ctas = _int32("num_ctas", num_ctas)
     args = [q.data_ptr(), kp, vp, ks, vs,
             _take("block_tables", block_tables, torch.int32, dev), mb,
             _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None,
@@ -746,7 +754,7 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
         _need_cuda("out", out, torch.bfloat16)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-    num_ctas = int(num_ctas)
+    num_ctas = _int32("num_ctas", num_ctas)
     args = [q.data_ptr(), T, _take("cu_q", cu_q, torch.int32, dev), kp, vp, ks, vs,
             _take("block_tables", block_tables, torch.int32, dev), mb,
             _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None, None, 0,
@@ -789,7 +797,7 @@ def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int,
     if mass.dim() != 3 or context_lens.shape != mass.shape[:1]:
         raise ValueError("mass must be [num_seqs, n_kv, max_tokens], context_lens [num_seqs]")
     B, n_kv, tokens = mass.shape
-    budget, recent = int(budget), int(recent)
+    budget, recent = _int32("budget", budget), _int32("recent", recent)
     if budget <= 0 or not 0 <= recent <= budget:
         raise ValueError("budget must be > 0 and recent within 0 .. budget")
     for nm, t, shape in (("keep", keep, (B, n_kv, budget)), ("keep_lens", keep_lens, (B,))):
@@ -830,7 +838,8 @@ def pa_evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     if block_tables.dim() != 2 or new_tables.dim() != 2 or keep.dim() != 3:
         raise ValueError("block_tables, new_tables must be [num_seqs, blocks], keep "
                          "[num_seqs, n_kv, budget]")
-    B, heads, budget = keep.shape
+    B, heads = keep.shape[:2]
+    budget = _int32("keep's budget", keep.shape[2])
     tables, mb = block_tables.shape
     news, nb = new_tables.shape
     if heads != g.n_kv or tables != B or news != B or keep_lens.shape != (B,):
@@ -1044,7 +1053,7 @@ class BlockAllocator:
     def allocate_private(self, n_tokens: int) -> np.ndarray:
         """Block table (int32 array) of fresh blocks for n_tokens rows that no prompt
         can share: the new home of a sequence that pa_evict_compact cuts."""
-        n_tokens = int(n_tokens)
+        n_tokens = _int32("n_tokens", n_tokens)
         cap = max(0, n_tokens + self.block_size - 1) // self.block_size
         table = np.empty(max(cap, 1), np.int32)
         n = ctypes.c_int32()

@@ -138,3 +138,11 @@ def test_private_blocks(lib):
     assert lib.pa_allocator_allocate_private(a._h, 40, p, 2, ctypes.byref(n_blocks)) == -2
     assert lib.pa_allocator_allocate_private(a._h, 40, None, 4, ctypes.byref(n_blocks)) == -1
     assert lib.pa_allocator_allocate_private(None, 40, p, 4, ctypes.byref(n_blocks)) == -1
+
+
+def test_private_blocks_of_more_tokens_than_32_bits_count():
+    """2^32 + 16 tokens are not 16."""
+    a = pa.BlockAllocator(8)
+    with pytest.raises(ValueError, match="32 bits"):
+        a.allocate_private((1 << 32) + 16)
+    assert a.num_free() == 8

@@ -225,6 +225,26 @@ def test_a_stream_s_larger_workspace_replaces_the_smaller_one():
         assert torch.cuda.memory_allocated() - before > larger // 4
 
 
+def test_numbers_beyond_32_bits_are_refused():
+    """Cut to their low bits they would be another budget, or another CTA count."""
+    mass = torch.rand(1, 1, 64, device=DEV)
+    cl = torch.tensor([64], dtype=torch.int32, device=DEV)
+    for kw in (dict(budget=(1 << 32) + 5), dict(budget=5, recent=1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            pa.pa_evict_select(mass, cl, **kw)
+    gen = torch.Generator().manual_seed(60)
+    bt, total, _ = make_tables(gen, [64])
+    pool = make_pool(gen, total, 1, 64, "bf16")
+    q = torch.randn(1, 1, 64, generator=gen).to(torch.bfloat16).to(DEV)
+    with pytest.raises(ValueError, match="32 bits"):
+        pa.pa_decode_mass(q, pool[0], pool[1], bt.to(DEV), cl, 0.1, mass,
+                          num_ctas=(1 << 32) + 1)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="32 bits"):
+        pa.pa_cross_attention(q, cu, pool[0], pool[1], bt.to(DEV), cl, 0.1,
+                              num_ctas=(1 << 32) + 1)
+
+
 def test_mass_of_shared_blocks_bad_blocks_and_bad_lengths():
     gen = torch.Generator().manual_seed(3)
     ctx = [40, 40, 100, 64, 30]
