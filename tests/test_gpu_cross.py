@@ -196,6 +196,26 @@ def test_non_finite_rows_stay_their_own():
     assert torch.equal(out[rest], want[rest])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
+def test_non_finite_rows_stay_their_own_in_every_pool(kv, d):
+    """Each row of a group of four that lie eight apart (a thread of the quantised softmax has
+    them) and its neighbours, in a unit of one half (90 rows) and in one of two (250)."""
+    ctx = [700, 333]
+    q, cu, pool, bt = case(kv, d, 1, 1, [90, 250], ctx, seed=13)
+    want = {c: run(q, cu, pool, bt, ctx, 0.1, num_ctas=c)[0] for c in (0, 1)}
+    for odd, value in (((3, 13, 49, 90 + 5, 90 + 140), float("nan")),
+                       ((11, 27, 60, 90 + 21, 90 + 200), float("inf")),
+                       ((19, 34, 89, 90, 90 + 249), -float("inf"))):
+        x = q.clone()
+        x[list(odd)] = value
+        for num_ctas in (0, 1):
+            out, st = run(x, cu, pool, bt, ctx, 0.1, num_ctas=num_ctas)
+            assert st == 0 and torch.isnan(out[list(odd)]).all()
+            rest = [i for i in range(340) if i not in odd]
+            assert torch.equal(out[rest], want[num_ctas][rest])
+
+
 @pytest.mark.parametrize("kv", ["bf16", "int8", "int4"])
 def test_reports(kv):
     ctx = [100, 300, 64, 50, 20]
