@@ -404,7 +404,11 @@ size_t pa_cross_workspace_size(pa_geom geom, int32_t num_ctas);
  * how the work was split. A bad block's tokens have weight 0; a sequence with
  * a bad context length keeps its masses. Two sequences that share blocks have
  * masses of their own. Every other argument and error is pa_decode's, plus
- * num_ctas (0: the default grid; > 0: the CTA count, as in pa_decode_ex). The
+ * num_ctas (0: pa_decode's default grid; > 0: the CTA count, as in pa_decode_ex);
+ * the output is pa_decode's, bit for bit, on the same grid. There is no form for
+ * steps of several tokens (pa_decode_mq: a prompt's own queries, a speculative
+ * verify), a window, sinks or shared prefixes (pa_decode_opt): the weights of
+ * such steps reach no mass. The
  * workspace is pa_decode_mass_workspace_size bytes: pa_decode's part, zeroed as
  * pa_decode_workspace_init says, and the scores, 4 bytes per query head and
  * block-table slot. The pages have no counterpart.

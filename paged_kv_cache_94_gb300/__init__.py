@@ -672,7 +672,8 @@ def pa_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     mass: float32 [B, n_kv, max_blocks * 16], entry j for the token at
     block_tables[b][j // 16], offset j % 16; the sums go to mass_out (default: in
     place). Entries at and behind a context's end are not written. Everything
-    else, and the result, as pa_decode.
+    else, and the result, as pa_decode without its options (window, sinks, shared
+    prefixes).
 
     The workspace holds a score per query head and block-table slot, 4 * B * n_h *
     max_blocks * 16 bytes (64 sequences, 32 heads, a table of 128K tokens: 1.07 GB),

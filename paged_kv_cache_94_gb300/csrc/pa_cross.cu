@@ -38,12 +38,12 @@
 // The softmax base of a row moves rarely (kMoveLog2), so O is rarely rescaled.
 //
 // Measured on a GB300 (g = 4, d_h 128, bf16): 8 prompts of 512..1024 tokens over
-// 4096..8192 keys 463 us, 1370 TFLOP/s, 0.70 of the measured bf16 matrix rate; a
-// buffer's chain (products 512 cycles, 290 until they are seen, scores 512, softmax
-// 1700) bounds a tile of 256 x 128 at 3350 cycles against 2048 of products. 48
-// sequences of 1..61 tokens over 200..4096 keys 106 us, 4200 GB/s, 0.63 of the
-// measured copy rate: 2700 cycles a tile, the K/V stream's own, and 30% of the time
-// in first loads, unit ends and merges.
+// 4096..8192 keys 616 us (680 back to back, under the power cap), 1030 TFLOP/s with each
+// product counted once, 0.53 of the measured bf16 matrix rate; a buffer's chain (the last
+// 64 keys' products, 290 cycles until they are seen, scores 512, softmax) bounds a tile of
+// 256 x 128 at 4650 cycles against 3072 of products. 48 sequences of 1..61 tokens over
+// 200..4096 keys 121 us, 3690 GB/s, 0.54 of the measured copy rate: the same chain, first
+// loads, unit ends and merges.
 #include "pa_decode.cuh"
 #include "pa_launch.h"
 #include "pa_tcgen05.cuh"
@@ -242,7 +242,11 @@ struct MergeState {
     }
 };
 
-// CTAs that take part: each range is as long as the longest item, so that each owns one.
+// CTAs that take part: each range is as long as the longest item. So a range that lies between
+// the first positions of a unit's first and last item holds an item's first position: every CTA
+// from the first item's owner to the last one's has an item of the unit, and each of them
+// leaves a record and arrives. A range that lies within a unit's charge owns nothing.
+static_assert(kWeight2 >= kWeight1, "the longest item");
 __device__ __forceinline__ int64_t line_ctas(const CrossParams &p, int64_t total)
 {
     return total == 0 ? 0 : max((int64_t)1, plan_ctas(p.num_ctas, total / kWeight2));

@@ -12,10 +12,11 @@
 //   execution.
 //   A row is 4 n bytes, read once: latency-bound. So a long row is cut over a
 //   cluster of up to 8 CTAs (counts joined in the first one's shared memory) and
-//   the keys stay in shared memory between the sweeps; rows too long for that
-//   read them again from L2. 512 rows of 900..4096 tokens: 17 us a call, 32 of
-//   32K..128K: 31 us (11 and 40 thousand cycles a CTA: loads, then six steps of
-//   which each is one or two barriers).
+//   the keys stay in shared memory between the sweeps; rows too long for that, by the
+//   stride of the masses, read them again from L2. 512 rows of 900..4096 tokens: 17 us a
+//   call (14 on the GPU, in two waves; 16 with a stride of 131072), 32 of 32K..128K: 31 us
+//   (11 and 40 thousand cycles a CTA: loads, then six steps of which each is one or two
+//   barriers).
 //
 // compact_kernel: row i of the new block table = row keep[i] of the old one,
 //   for K, V, their scales and the masses. Bound by HBM: each kept row is read
@@ -38,7 +39,7 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kKeys = 48; // keys of a thread that fit in shared memory, two CTAs per SM
+constexpr int kKeys = 48; // keys of a thread kept in shared memory (up to 47: two CTAs per SM)
 
 // Masses as unsigned integers of the same order. -0 equals +0; NaN lies below
 // everything, so a token whose mass is not a number goes first.
