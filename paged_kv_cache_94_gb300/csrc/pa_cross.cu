@@ -41,7 +41,7 @@
 // 4096..8192 keys 616 us (680 back to back, under the power cap), 1030 TFLOP/s with each
 // product counted once, 0.53 of the measured bf16 matrix rate; a buffer's chain (the last
 // 64 keys' products, 290 cycles until they are seen, scores 512, softmax) bounds a tile of
-// 256 x 128 at 4650 cycles against 3072 of products. 48 sequences of 1..61 tokens over
+// 256 x 128 at 4650 cycles against about 3100 of products. 48 sequences of 1..61 tokens over
 // 200..4096 keys 121 us, 3690 GB/s, 0.54 of the measured copy rate: the same chain, first
 // loads, unit ends and merges.
 #include "pa_decode.cuh"
