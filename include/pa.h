@@ -483,6 +483,48 @@ pa_status pa_evict_compact(void *k_cache, void *v_cache, float *k_scale, float *
                            int32_t *dev_status, void *stream);
 
 /*
+ * pa_rope_write -- rotary positions with the append: queries and keys are turned by
+ * their tokens' positions, keys and values written to the pool as pa_cache_write does.
+ *
+ * Pair i < num_pairs of every head of q and k turns by
+ *     angle = positions[axis[i]][t] * inv_freq[i]
+ *     (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * its values being d = i and i + num_pairs (adjacent 0) or 2 i and 2 i + 1 (adjacent 1).
+ * Values from d = 2 * num_pairs on, and v, stay as they are. Angles are exact for every
+ * int32 position (an inv_freq counts as a 64-bit fraction of a turn); sines, cosines and
+ * the rotation are in fp32. A bf16 pool and out take the result rounded once; INT8 and
+ * INT4 pools take the codes of the fp32 result, with pa_cache_write's quantiser.
+ *
+ *   q, k, v        bf16 [num_tokens][n_h or n_kv][d_h], the rows of a token dense, from
+ *                  token to token q_stride, k_stride, v_stride elements (multiples of 8, at
+ *                  least a token's rows: PA_ERR_ALIGNMENT, PA_ERR_SHAPE), so that they may
+ *                  be parts of one projection's output
+ *   num_tokens     0 .. 2^31 - 1 (0 enqueues nothing)
+ *   positions      int32 [n_axes][num_tokens]: of each token on each axis (one for text;
+ *                  time, height, width for images and video); may be negative
+ *   n_axes         1 .. 4
+ *   inv_freq       double [num_pairs] (device): radians per position, any scaling for long
+ *                  contexts included; one that is not finite gives NaN
+ *   axis           int32 [num_pairs] (device), or NULL: axis 0 for all. A pair whose axis
+ *                  is not there stays as it is and sets PA_DEV_BAD_CONTEXT.
+ *   num_pairs      a multiple of 8 (PA_ERR_UNSUPPORTED), up to d_h / 2
+ *   amplitude      factor on what is turned, 1 for none
+ *   slot_mapping   int64 [num_tokens]: as for pa_cache_write; < 0 writes no K and V (q is
+ *                  turned all the same)
+ *   out            bf16 [num_tokens][n_h][d_h] (written); q itself, where q is dense, or
+ *                  memory that meets none of q's, k's and v's (PA_ERR_SHAPE)
+ *   pool, scales, dev_status  as for pa_cache_write
+ * n_h + 2 n_kv up to 65536. The pages have no counterpart.
+ */
+pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, int64_t num_tokens,
+                        const int32_t *positions, int32_t n_axes, const double *inv_freq,
+                        const int32_t *axis, int32_t num_pairs, int32_t adjacent,
+                        float amplitude, const int64_t *slot_mapping, void *out, void *k_cache,
+                        void *v_cache, float *k_scale, float *v_scale, pa_geom geom,
+                        int32_t *dev_status, void *stream);
+
+/*
  * pa_sink_write -- store bf16 attention-sink rows of new tokens.
  *
  * For each row t with 0 <= positions[t] < n_sink and 0 <= seq_rows[t] <

@@ -50,6 +50,7 @@ EXPORTED = ["pa_cache_write", "pa_decode_workspace_size", "pa_decode_workspace_i
             "pa_kv_read_probe", "pa_share_groups",
             "pa_decode_mass", "pa_decode_mass_workspace_size", "pa_evict_select",
             "pa_evict_compact", "pa_cross_attention", "pa_cross_workspace_size",
+            "pa_rope_write",
             # host block manager (include/pa_alloc.h)
             "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate_prompt",
             "pa_allocator_allocate_private",
@@ -143,6 +144,9 @@ def _lib():
         lib.pa_cross_attention.restype = ctypes.c_int
         lib.pa_cross_attention.argtypes = [P, i64, P, P, P, P, P, P, i32, P, i32, f32, P, P, sz,
                                            pa_geom, P, P, i32]
+        lib.pa_rope_write.restype = ctypes.c_int
+        lib.pa_rope_write.argtypes = [P, i64, P, i64, P, i64, i64, P, i32, P, P, i32, i32, f32, P, P,
+                                      P, P, P, P, pa_geom, P, P]
         lib.pa_evict_select.restype = ctypes.c_int
         lib.pa_evict_select.argtypes = [P, i64, P, i32, i32, i32, i32, P, P, P, P]
         lib.pa_evict_compact.restype = ctypes.c_int
@@ -782,6 +786,76 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
         args[14] = workspace.numel() * workspace.element_size()
         return _issue(_lib().pa_cross_attention, args, 17, "pa_cross_attention", out, handle, stream,
                       dev, owned)
+
+
+def _rows_of(name: str, t: torch.Tensor, tokens: int, heads: int, d: int, device):
+    """Pointer of rows [tokens, heads, d] (bf16) whose tokens are dense, and the elements from
+    token to token."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.Tensor of torch.bfloat16")
+    if t.get_device() != device.index:
+        raise ValueError(f"{name} must be on {device} (there is no CPU path)")
+    if t.shape != (tokens, heads, d):
+        raise ValueError(f"{name} must be {[tokens, heads, d]}, got {list(t.shape)}")
+    step, head, one = t.stride()
+    if one != 1 or (head != d and heads > 1) or (step < heads * d and tokens > 1):
+        raise ValueError(f"{name}: the rows of a token must be dense")
+    return t.data_ptr(), step if tokens > 1 else heads * d
+
+
+def pa_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                  inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, axis: Optional[torch.Tensor] = None,
+                  adjacent: bool = False, amplitude: float = 1.0,
+                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                  stream=None, prepare: bool = False):
+    """Turn queries and keys by their positions, and append K and V to the pool
+    (pa_cache_write of the turned keys, without rounding them in between).
+
+    q [T, n_h, d_h], k, v [T, n_kv, d_h] bf16, each token's rows dense (views of one
+    projection's output will do) -> the turned q [T, n_h, d_h]. positions int32 [T] or
+    [n_axes, T] (time, height, width: up to 4 axes); inv_freq float64 [pairs], radians per
+    position of each pair of values, pairs a multiple of 8 up to d_h / 2; axis int32
+    [pairs], the axis each pair goes by (default: the first). Pairs are values (i,
+    i + pairs), or with adjacent (2 i, 2 i + 1); the values behind them stay. amplitude
+    multiplies what is turned. slot_mapping int64 [T] as for pa_cache_write (< 0: no K, V).
+    out may be q where q is contiguous."""
+    _need_cuda("k_cache", k_cache)
+    dev = k_cache.device
+    if q.dim() != 3 or positions.dim() not in (1, 2) or inv_freq.dim() != 1:
+        raise ValueError("q must be [num_tokens, n_h, d_h], positions [num_tokens] or "
+                         "[n_axes, num_tokens], inv_freq [pairs]")
+    T, n_h, d = q.shape
+    g, kp, vp, ks, vs = _pool(k_cache, v_cache, k_scale, v_scale, n_h, dev)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    pairs = inv_freq.shape[0]
+    if d != g.d_h or positions.shape[-1] != T or slot_mapping.shape != (T,):
+        raise ValueError("q, positions, slot_mapping and the pool disagree on num_tokens or d_h")
+    if not 1 <= axes <= 4:
+        raise ValueError("positions must have 1 to 4 axes")
+    if pairs % 8 or not 8 <= pairs <= d // 2:
+        raise ValueError("inv_freq must have a multiple of 8 of pairs, up to d_h / 2")
+    if axis is not None and axis.shape != (pairs,):
+        raise ValueError("axis must be [pairs]")
+    qp, q_step = _rows_of("q", q, T, n_h, d, dev)
+    kn, k_step = _rows_of("k", k, T, g.n_kv, d, dev)
+    vn, v_step = _rows_of("v", v, T, g.n_kv, d, dev)
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    args = [qp, q_step, kn, k_step, vn, v_step, T, _take("positions", positions, torch.int32, dev),
+            axes, _take("inv_freq", inv_freq, torch.float64, dev),
+            _opt("axis", axis, torch.int32, dev), pairs, int(bool(adjacent)), float(amplitude),
+            _take("slot_mapping", slot_mapping, torch.int64, dev), None, kp, vp, ks, vs, g,
+            _opt("dev_status", dev_status, torch.int32, dev), None]
+    with _on(dev, stream):
+        owned = _Owned(dev) if prepare else None
+        if out is None:
+            out = (owned.empty((T, n_h, d), q.dtype) if prepare else
+                   torch.empty((T, n_h, d), dtype=q.dtype, device=dev))
+        args[15] = _take("out", out, torch.bfloat16, dev)
+        return _issue(_lib().pa_rope_write, args, 22, "pa_rope_write", out, _stream_handle(dev),
+                      stream, dev, owned)
 
 
 def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int, recent: int = 0,

@@ -40,6 +40,7 @@ SOURCES = [
     "pa_decode_mass_int8.cu",
     "pa_decode_mass_int4.cu",
     "pa_cross.cu",
+    "pa_rope.cu",
     "pa_mass.cu",
     "pa_evict.cu",
     "pa_share.cu",

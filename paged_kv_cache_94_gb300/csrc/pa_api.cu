@@ -768,6 +768,87 @@ pa_status pa_decode_mass(const void *q, const void *k_cache, const void *v_cache
                        dev_status, stream, num_ctas, nullptr, 1, &ma);
 }
 
+pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, int64_t num_tokens,
+                        const int32_t *positions, int32_t n_axes, const double *inv_freq,
+                        const int32_t *axis, int32_t num_pairs, int32_t adjacent,
+                        float amplitude, const int64_t *slot_mapping, void *out, void *k_cache,
+                        void *v_cache, float *k_scale, float *v_scale, pa_geom geom,
+                        int32_t *dev_status, void *stream)
+{
+    const NvtxRange range("pa_rope_write");
+    pa_status st = check_geom(geom);
+    if (st != PA_OK)
+        return st;
+    if (num_tokens < 0 || n_axes < 1 || n_axes > 4 || num_pairs < 1 ||
+        num_pairs > geom.d_h / 2 || (adjacent != 0 && adjacent != 1))
+        return PA_ERR_SHAPE;
+    const int64_t rows = (int64_t)geom.n_h + 2 * (int64_t)geom.n_kv;
+    if (num_pairs % 8 != 0 || rows > (1 << 16) || num_tokens >= (int64_t(1) << 31))
+        return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0)
+        return PA_OK;
+    if (!q || !k || !v || !positions || !inv_freq || !slot_mapping || !out || !k_cache || !v_cache)
+        return PA_ERR_NULL;
+    const bool i8 = geom.kv_dtype != PA_KV_BF16; // INT8 or INT4: fp32 scales
+    if (i8 && (!k_scale || !v_scale))
+        return PA_ERR_NULL;
+    if (!i8 && (k_scale || v_scale))
+        return PA_ERR_SHAPE;
+    if (q_stride < (int64_t)geom.n_h * geom.d_h || k_stride < (int64_t)geom.n_kv * geom.d_h ||
+        v_stride < (int64_t)geom.n_kv * geom.d_h)
+        return PA_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || q_stride % 8 || k_stride % 8 ||
+        v_stride % 8 || !aligned(positions, 4) || !aligned(axis, 4) || !aligned(inv_freq, 8) ||
+        !aligned(slot_mapping, 8) || (i8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
+        return PA_ERR_ALIGNMENT;
+    // out is q itself, or apart from all that is read
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), row = (uintptr_t)geom.d_h * 2;
+    const uintptr_t o1 = o0 + (uintptr_t)num_tokens * geom.n_h * row;
+    auto meets = [&](const void *x, int64_t stride, int heads) {
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(x);
+        return x0 < o1 && o0 < x0 + (uintptr_t)(num_tokens - 1) * stride * 2 + heads * row;
+    };
+    const bool in_place = out == q && (q_stride == (int64_t)geom.n_h * geom.d_h || num_tokens == 1);
+    if ((!in_place && meets(q, q_stride, geom.n_h)) || meets(k, k_stride, geom.n_kv) ||
+        meets(v, v_stride, geom.n_kv))
+        return PA_ERR_SHAPE;
+    int dev, sms;
+    if ((st = current_device(dev, sms)) != PA_OK)
+        return st;
+    pa::RopeArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.num_tokens = num_tokens;
+    a.num_blocks = geom.num_blocks;
+    a.positions = positions;
+    a.axis = axis;
+    a.inv_freq = inv_freq;
+    a.slots = slot_mapping;
+    a.out = out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.dev_status = dev_status;
+    a.n_axes = n_axes;
+    a.pairs = num_pairs;
+    a.adjacent = adjacent;
+    a.n_h = geom.n_h;
+    a.n_kv = geom.n_kv;
+    a.d_h = geom.d_h;
+    a.kind = geom.kv_dtype;
+    a.amplitude = amplitude;
+    return pa::launch_rope_write(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
 size_t pa_cross_workspace_size(pa_geom geom, int32_t num_ctas)
 {
     int dev, sms;

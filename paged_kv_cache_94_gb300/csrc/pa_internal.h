@@ -78,6 +78,21 @@ size_t cross_workspace_bytes(int d_h, int num_ctas);
 cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CrossArgs &a, cudaStream_t stream);
 
+// Rotary positions with the append (pa_rope.cu).
+struct RopeArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, num_tokens, num_blocks;
+    const int32_t *positions, *axis;
+    const double *inv_freq;
+    const int64_t *slots;
+    void *out, *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    int32_t *dev_status;
+    int n_axes, pairs, adjacent, n_h, n_kv, d_h, kind;
+    float amplitude;
+};
+cudaError_t launch_rope_write(const RopeArgs &a, int sms, cudaStream_t stream);
+
 // Eviction by accumulated attention weight (pa_evict.cu).
 cudaError_t launch_evict_select(const float *mass, int64_t stride, const int32_t *context_lens,
                                 int num_seqs, int n_kv, int budget, int recent, int32_t *keep,
