@@ -525,6 +525,31 @@ pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t 
                         int32_t *dev_status, void *stream);
 
 /*
+ * pa_window_decode -- pa_decode over the last `window` tokens of each sequence and its
+ * first n_first ones, which stay visible behind the window.
+ *     attended: j < ctx_b with j >= ctx_b - window or j < n_first (window 0: all)
+ * (pa_decode_opt's window has no first tokens: its n_sink are bf16 rows of positions inside
+ * the window.) Block-table entries of blocks wholly between the two are not read: a
+ * windowed cache may have given them back.
+ *
+ *   window, n_first  >= 0 (PA_ERR_SHAPE)
+ *   num_ctas         0: one wave of resident CTAs; > 0: that many
+ * Every other argument and error is pa_decode's; the workspace is
+ * pa_window_decode_workspace_size(geom, num_seqs, num_ctas) bytes, zeroed as
+ * pa_decode_workspace_init says.
+ */
+pa_status pa_window_decode(const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, int32_t num_seqs, float scale,
+                           int32_t window, int32_t n_first, void *out, void *workspace,
+                           size_t workspace_bytes, pa_geom geom, int32_t *dev_status,
+                           void *stream, int32_t num_ctas);
+
+/* Workspace bytes pa_window_decode needs on the current device; 0 if an argument is invalid. */
+size_t pa_window_decode_workspace_size(pa_geom geom, int32_t num_seqs, int32_t num_ctas);
+
+/*
  * pa_sink_write -- store bf16 attention-sink rows of new tokens.
  *
  * For each row t with 0 <= positions[t] < n_sink and 0 <= seq_rows[t] <

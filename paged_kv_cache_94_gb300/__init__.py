@@ -50,7 +50,7 @@ EXPORTED = ["pa_cache_write", "pa_decode_workspace_size", "pa_decode_workspace_i
             "pa_kv_read_probe", "pa_share_groups",
             "pa_decode_mass", "pa_decode_mass_workspace_size", "pa_evict_select",
             "pa_evict_compact", "pa_cross_attention", "pa_cross_workspace_size",
-            "pa_rope_write",
+            "pa_rope_write", "pa_window_decode", "pa_window_decode_workspace_size",
             # host block manager (include/pa_alloc.h)
             "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate_prompt",
             "pa_allocator_allocate_private",
@@ -147,6 +147,10 @@ def _lib():
         lib.pa_rope_write.restype = ctypes.c_int
         lib.pa_rope_write.argtypes = [P, i64, P, i64, P, i64, i64, P, i32, P, P, i32, i32, f32, P, P,
                                       P, P, P, P, pa_geom, P, P]
+        lib.pa_window_decode_workspace_size.restype = sz
+        lib.pa_window_decode_workspace_size.argtypes = [pa_geom, i32, i32]
+        lib.pa_window_decode.restype = ctypes.c_int
+        lib.pa_window_decode.argtypes = dec[:10] + [i32, i32] + dec[10:] + [i32]
         lib.pa_evict_select.restype = ctypes.c_int
         lib.pa_evict_select.argtypes = [P, i64, P, i32, i32, i32, i32, P, P, P, P]
         lib.pa_evict_compact.restype = ctypes.c_int
@@ -856,6 +860,60 @@ def pa_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
         args[15] = _take("out", out, torch.bfloat16, dev)
         return _issue(_lib().pa_rope_write, args, 22, "pa_rope_write", out, _stream_handle(dev),
                       stream, dev, owned)
+
+
+def pa_window_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                     window: int = 0, n_first: int = 0, out: Optional[torch.Tensor] = None,
+                     k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None, num_ctas: int = 0,
+                     prepare: bool = False):
+    """pa_decode over the last `window` tokens of each sequence (0: all) and its first
+    n_first ones. q [B, n_h, d_h] bf16 -> out of q's shape. Blocks wholly between the two
+    are not read: their table entries may be anything. Everything else as pa_decode
+    without its options."""
+    _need_cuda("q", q, torch.bfloat16)
+    dev = q.device
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [num_seqs, n_h, d_h], block_tables [num_seqs, max_blocks]")
+    B, n_h, d = q.shape
+    tables, mb = block_tables.shape
+    g, kp, vp, ks, vs = _pool(k_cache, v_cache, k_scale, v_scale, n_h, dev)
+    if d != g.d_h or tables != B or context_lens.shape != (B,):
+        raise ValueError("q, block_tables, context_lens disagree on num_seqs or d_h")
+    if out is not None:
+        _need_cuda("out", out, torch.bfloat16)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    num_ctas = _int32("num_ctas", num_ctas)
+    args = [q.data_ptr(), kp, vp, ks, vs,
+            _take("block_tables", block_tables, torch.int32, dev), mb,
+            _take("context_lens", context_lens, torch.int32, dev), B, float(scale),
+            _int32("window", window), _int32("n_first", n_first), None, None, 0, g,
+            _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
+    with _on(dev, stream), _STREAM_LOCK:
+        handle = _stream_handle(dev)
+        owned = _Owned(dev) if prepare else None
+        if out is None:
+            out = owned.empty(q.shape, q.dtype) if prepare else torch.empty_like(q)
+        if workspace is None:
+            key = ("window", dev.index, g.num_blocks, n_h, g.n_kv, d, g.kv_dtype, B, num_ctas)
+            nbytes = _WS_SIZES.get(key)
+            if nbytes is None:
+                nbytes = _lib().pa_window_decode_workspace_size(g, B, num_ctas)
+                if nbytes == 0:
+                    raise PAError(-4, "pa_window_decode_workspace_size")
+                _WS_SIZES[key] = nbytes
+            counters = _counter_bytes(g, B)
+            workspace = (owned.workspace(nbytes, counters) if prepare else
+                         _stream_workspace("window", nbytes, counters, dev, handle))
+        args[12] = _take("out", out, torch.bfloat16, dev)
+        args[13] = _take("workspace", workspace, workspace.dtype, dev)
+        args[14] = workspace.numel() * workspace.element_size()
+        return _issue(_lib().pa_window_decode, args, 17, "pa_window_decode", out, handle, stream,
+                      dev, owned)
 
 
 def pa_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, budget: int, recent: int = 0,

@@ -39,6 +39,9 @@ SOURCES = [
     "pa_decode_mass_bf16.cu",
     "pa_decode_mass_int8.cu",
     "pa_decode_mass_int4.cu",
+    "pa_decode_window_bf16.cu",
+    "pa_decode_window_int8.cu",
+    "pa_decode_window_int4.cu",
     "pa_cross.cu",
     "pa_rope.cu",
     "pa_mass.cu",

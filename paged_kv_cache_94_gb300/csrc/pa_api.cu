@@ -198,6 +198,10 @@ struct MassArgs {
     float *mass_out;
 };
 
+struct WindowArgs {
+    int32_t window, n_first;
+};
+
 // Shared memory and resident CTAs per SM of the shared-prefix kernel for a
 // batch (its 2 * num_seqs units' prefix arrays grow with the batch);
 // PA_ERR_UNSUPPORTED when not even one CTA fits on an SM.
@@ -339,11 +343,13 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
                       const int32_t *context_lens, int32_t num_seqs, float scale, void *out,
                       void *workspace, size_t workspace_bytes, pa_geom g, int32_t *dev_status,
                       void *stream, int32_t num_ctas, const pa_decode_opts *opts = nullptr,
-                      int nq = 1, const MassArgs *ma = nullptr)
+                      int nq = 1, const MassArgs *ma = nullptr, const WindowArgs *wa = nullptr)
 {
     pa_status st = check_geom(g);
     if (st != PA_OK)
         return st;
+    if (wa && (wa->window < 0 || wa->n_first < 0))
+        return PA_ERR_SHAPE;
     const pa_decode_opts none = {0, 0, nullptr, nullptr, 0, 0, 0};
     const pa_decode_opts &o = opts ? *opts : none;
     if (o.window < 0 || o.n_sink < 0 || o.n_sink > 16 || o.reserved != 0 ||
@@ -383,7 +389,9 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
         return PA_ERR_ALIGNMENT;
 
     const DecodeKernel *kd =
-        ma ? pa::find_mass_kernel(g.kv_dtype, g.d_h, group_of(g)) : kernel_for(g, nq);
+        ma   ? pa::find_mass_kernel(g.kv_dtype, g.d_h, group_of(g))
+        : wa ? pa::find_window_kernel(g.kv_dtype, g.d_h, group_of(g))
+             : kernel_for(g, nq);
     if (!kd)
         return PA_ERR_UNSUPPORTED;
     int dev, sms, per;
@@ -436,7 +444,8 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
     p.max_blocks = max_blocks;
     p.num_ctas = grid;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    p.window = o.window;
+    p.window = wa ? wa->window : o.window;
+    p.n_first = wa ? wa->n_first : 0;
     p.n_sink = o.n_sink;
     p.sink_k = static_cast<const __nv_bfloat16 *>(o.n_sink > 0 ? o.sink_k : nullptr);
     p.sink_v = static_cast<const __nv_bfloat16 *>(o.n_sink > 0 ? o.sink_v : nullptr);
@@ -545,6 +554,17 @@ const DecodeKernel *find_decode_kernel_int4_mq(int d_h, int group, int nq)
 {
     return d_h == 128 ? find_decode_kernel_int4_mq_d128(group, nq)
                       : d_h == 64 ? find_decode_kernel_int4_mq_d64(group, nq) : nullptr;
+}
+
+const DecodeKernel *find_window_kernel_bf16(int d_h, int group);
+const DecodeKernel *find_window_kernel_int8(int d_h, int group);
+const DecodeKernel *find_window_kernel_int4(int d_h, int group);
+
+const DecodeKernel *find_window_kernel(int kind, int d_h, int group)
+{
+    return kind == PA_KV_BF16   ? find_window_kernel_bf16(d_h, group)
+           : kind == PA_KV_INT8 ? find_window_kernel_int8(d_h, group)
+                                : find_window_kernel_int4(d_h, group);
 }
 
 const DecodeKernel *find_decode_kernel_int8(int d_h, int group)
@@ -766,6 +786,35 @@ pa_status pa_decode_mass(const void *q, const void *k_cache, const void *v_cache
     return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
                        context_lens, num_seqs, scale, out, workspace, workspace_bytes, geom,
                        dev_status, stream, num_ctas, nullptr, 1, &ma);
+}
+
+size_t pa_window_decode_workspace_size(pa_geom geom, int32_t num_seqs, int32_t num_ctas)
+{
+    if (check_geom(geom) != PA_OK || num_seqs < 0 || num_seqs > kMaxSeqs || num_ctas < 0)
+        return 0;
+    const DecodeKernel *kd = pa::find_window_kernel(geom.kv_dtype, geom.d_h, group_of(geom));
+    int dev, sms, per;
+    if (!kd)
+        return 0;
+    if (num_ctas == 0 && (current_device(dev, sms) != PA_OK ||
+                          ctas_per_sm(kd, kd->smem_bytes(num_seqs), per) != PA_OK))
+        return 0;
+    return workspace_bytes_for(geom, num_seqs, num_ctas > 0 ? num_ctas : sms * per);
+}
+
+pa_status pa_window_decode(const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, int32_t num_seqs, float scale,
+                           int32_t window, int32_t n_first, void *out, void *workspace,
+                           size_t workspace_bytes, pa_geom geom, int32_t *dev_status,
+                           void *stream, int32_t num_ctas)
+{
+    const NvtxRange range("pa_window_decode");
+    const WindowArgs wa = {window, n_first};
+    return decode_impl(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
+                       context_lens, num_seqs, scale, out, workspace, workspace_bytes, geom,
+                       dev_status, stream, num_ctas, nullptr, 1, nullptr, &wa);
 }
 
 pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -93,10 +93,13 @@ struct DecodeParams {
     // row's softmax base and 1 / sum to ml[b][head].
     float *scores;
     float2 *ml;
+    // A window with first tokens (PASS 1): besides the window, positions < n_first are attended.
+    int32_t n_first;
 };
 
-// Pass 0: decode of each sequence; pass 2: shared-prefix groups, then each
-// sequence's remaining blocks. Block-table row of "sequence" s.
+// Pass 0: decode of each sequence; pass 1: the same over a window and the
+// sequence's first tokens; pass 2: shared-prefix groups, then each sequence's
+// remaining blocks. Block-table row of "sequence" s.
 template <int PASS>
 __device__ __forceinline__ int32_t seq_table_row(const DecodeParams &p, int s)
 {
@@ -128,6 +131,21 @@ __device__ __forceinline__ int32_t window_start(const DecodeParams &p, int32_t c
 __device__ __forceinline__ int32_t seq_first_block(const DecodeParams &p, int32_t ctx)
 {
     return window_start(p, ctx) / kBlockTokens;
+}
+
+// Pass 1 reads a sequence as if its blocks between those of its first tokens and
+// its window's were not there: virtual block i is block i up to the former and
+// block i + skipped_blocks() behind them. What a token does not see is then one
+// hole, [n_first, the window's start), of at most 30 virtual positions: the rest of
+// the last block of first tokens and the front of the window's first block.
+__device__ __forceinline__ int32_t kept_blocks(const DecodeParams &p)
+{
+    return p.n_first / kBlockTokens + (p.n_first % kBlockTokens ? 1 : 0);
+}
+
+__device__ __forceinline__ int32_t skipped_blocks(const DecodeParams &p, int32_t ctx)
+{
+    return max(0, seq_first_block(p, ctx) - kept_blocks(p));
 }
 
 __device__ __forceinline__ void flag_error(int32_t *dev_status, int32_t bit)
@@ -205,7 +223,8 @@ __device__ __forceinline__ void prefix_blocks(const DecodeParams &p, int32_t *P,
                         flag_error(p.dev_status, PA_DEV_BAD_CONTEXT_BIT);
                 } else {
                     // blocks from the first one the sequence reads (window / shared prefix)
-                    v = (ctx + kBlockTokens - 1) / kBlockTokens - seq_first_block(p, ctx);
+                    v = (ctx + kBlockTokens - 1) / kBlockTokens -
+                        (PASS == 1 ? skipped_blocks(p, ctx) : seq_first_block(p, ctx));
                 }
             }
         }
@@ -973,6 +992,21 @@ __device__ __forceinline__ void load_item(const DecodeParams &p, const int32_t *
     locate_item(x, P, p.num_seqs, p.n_kv, b, kvh, i, nb);
     // first block of the item, and (BPI > 1) the blocks the unit reads
     int first = i * BPI, nblk = 0;
+    if constexpr (PASS == 1) {
+        const int32_t ctx = __ldg(p.context_lens + b), skip = skipped_blocks(p, ctx);
+        const int32_t kept = kept_blocks(p);
+        nblk = (ctx + kBlockTokens - 1) / kBlockTokens - skip;
+        const int32_t *row = p.block_tables + (size_t)b * p.max_blocks;
+#pragma unroll
+        for (int j = 0; j < BPI; ++j) {
+            const int v = first + j;
+            const bool present = j == 0 || v < nblk;
+            phys[j] = present ? __ldg(row + (v < kept ? v : v + skip)) : -1;
+            if (!present)
+                kvh |= 1 << (16 + j);
+        }
+        return;
+    }
     if constexpr (PASS == 0) {
         if (p.window > 0 || BPI > 1) {
             const int32_t ctx = __ldg(p.context_lens + b);

@@ -140,11 +140,12 @@ struct Bf16Policy {
     // One 16-token block: K tile at kt, V tile at kt + TILE (shared addresses).
     // Rows [lo, valid) of the block are attended; the others are masked. rem =
     // ctx - the block's first position (the multi-query causal limit). MASS:
-    // the attended tokens' scores also go to srow[token][GQ].
-    template <bool MASS = false>
+    // the attended tokens' scores also go to srow[token][GQ]. HOLE: rows [0, valid)
+    // are attended but for the hole [lo, hole_end).
+    template <bool MASS = false, bool HOLE = false>
     __device__ static void compute(State &st, uint32_t kt, uint32_t /*extra*/, int lo, int valid,
                                    int rem, float scale_log2, uint32_t /*mask: 1*/,
-                                   float *srow = nullptr)
+                                   float *srow = nullptr, int hole_end = 0)
     {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
         const int mi = lane >> 3, rr = lane & 7;
@@ -175,7 +176,10 @@ struct Bf16Policy {
         }
 
         // ---- online softmax (columns = heads; rows = tokens gid, gid+8)
-        const bool lo_ok = gid >= lo && gid < valid, hi_ok = gid + 8 >= lo && gid + 8 < valid;
+        auto in = [&](int t) {
+            return (HOLE ? t < lo || t >= hole_end : t >= lo) && t < valid;
+        };
+        const bool lo_ok = in(gid), hi_ok = in(gid + 8);
         uint32_t pb0[NT], pb1[NT], pl0[NT], pl1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -249,9 +253,9 @@ struct Bf16Policy {
             pl1[nt] = movmatrix_trans(r1);
         }
 
-        // ---- O^T += V^T P^T. Rows of V outside [lo, valid) may hold anything
+        // ---- O^T += V^T P^T. Rows of V that are not attended may hold anything
         // (even NaN): their operand halves are zeroed, since 0 * NaN is NaN.
-        if (lo == 0 && valid == kBlockTokens) {
+        if ((HOLE ? lo >= hole_end : lo == 0) && valid == kBlockTokens) {
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
                 uint32_t a0, a1, a2, a3;
@@ -264,7 +268,6 @@ struct Bf16Policy {
             }
         } else {
             const int t0 = 2 * t4;
-            auto in = [&](int t) { return t >= lo && t < valid; };
             const uint32_t mlo = (in(t0) ? 0x0000ffffu : 0u) | (in(t0 + 1) ? 0xffff0000u : 0u);
             const uint32_t mhi = (in(t0 + 8) ? 0x0000ffffu : 0u) | (in(t0 + 9) ? 0xffff0000u : 0u);
 #pragma unroll
@@ -332,7 +335,8 @@ namespace pa {
 // ---------------------------------------------------------------------------
 // The kernel: split, ring, segments, merge.
 // ---------------------------------------------------------------------------
-// PASS 0: decode of each sequence. PASS 2: shared-prefix decode, the groups'
+// PASS 0: decode of each sequence. PASS 1: the same over a window and the
+// sequence's first tokens. PASS 2: shared-prefix decode, the groups'
 // shared blocks (all query rows of the group at once) and then every
 // sequence's remaining blocks, in one launch. MASS (pass 0 only): the scores
 // and softmax bases also go to p.scores and p.ml.
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
     constexpr int TOK = BPI * kBlockTokens;      // tokens per item
     prefix_blocks<NW * 32, PASS, BPI>(p, P, misc + 8);
     __syncthreads();
-    if constexpr (PASS == 0) {
+    if constexpr (PASS != 2) {
         zero_empty_sequences<D, Pol::NQ>(p, P, n_h);
     } else if constexpr (PASS == 2) {
         // sequences with no blocks (ctx 0 or invalid) sit after the group units
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
     const int64_t Wv = virt_total(p, P);
     int64_t G = plan_ctas(p.num_ctas, Wv);
     int64_t lo, hi;
-    const int64_t U = PASS == 0 ? whole_unit_grid<NW * 32>(p, P, G, misc + 8) : 0;
+    const int64_t U = PASS != 2 ? whole_unit_grid<NW * 32>(p, P, G, misc + 8) : 0;
     if (U > 0) { // one CTA per unit: every segment is a whole unit
         if ((int64_t)blockIdx.x >= U)
             return;
@@ -503,8 +507,8 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
         locate_item(seg_lo, P, p.num_seqs, p.n_kv, b, kvh, i0, nb);
         Pol::prefetch_q(st, p, rows(b, kvh));
     }
-    // the next segment's context length, loaded with its q (pass 0)
-    int32_t ctx_next = (PASS == 0 && seg_lo < hi) ? __ldg(p.context_lens + b) : 0;
+    // the next segment's context length, loaded with its q (passes 0 and 1)
+    int32_t ctx_next = (PASS != 2 && seg_lo < hi) ? __ldg(p.context_lens + b) : 0;
     while (seg_lo < hi) {
         const int i0_cur = i0;
         const int64_t unit_start = seg_lo - i0;
@@ -525,6 +529,12 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
                 ctx = __ldg(p.context_lens + (b - p.num_real));
                 fb = __ldg(p.skip + (b - p.num_real));
             }
+        } else if constexpr (PASS == 1) { // virtual positions; [pool_from, ws) is the hole
+            const int32_t gone = skipped_blocks(p, ctx_next) * kBlockTokens;
+            ctx = ctx_next - gone;
+            ws = window_start(p, ctx_next) - gone;
+            pool_from = min(p.n_first, ws);
+            fb = 0;
         } else {
             ctx = ctx_next;
             ws = window_start(p, ctx);
@@ -558,6 +568,13 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
                     Pol::template compute<true>(st, ring_base + (uint32_t)(cstage * Pol::STAGE),
                                                 extra_base + (uint32_t)(cstage * Pol::EXTRA), lo,
                                                 valid, rem, p.scale_log2, (uint32_t)mask, srow);
+                } else if constexpr (PASS == 1) {
+                    // the hole within the item
+                    const int h1 = ws > t0 ? (int)min(ws - t0, TOK) : 0;
+                    Pol::template compute<false, true>(
+                        st, ring_base + (uint32_t)(cstage * Pol::STAGE),
+                        extra_base + (uint32_t)(cstage * Pol::EXTRA), lo, valid, rem,
+                        p.scale_log2, (uint32_t)mask, nullptr, h1);
                 } else if (lo < valid)
                     Pol::compute(st, ring_base + (uint32_t)(cstage * Pol::STAGE),
                                  extra_base + (uint32_t)(cstage * Pol::EXTRA), lo, valid, rem,
@@ -586,7 +603,7 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
         if (seg_hi < hi) {
             locate_item(seg_hi, P, p.num_seqs, p.n_kv, b, kvh, i0, nb);
             Pol::prefetch_q(st, p, rows(b, kvh));
-            if constexpr (PASS == 0)
+            if constexpr (PASS != 2)
                 ctx_next = __ldg(p.context_lens + b);
         }
         Pol::to_merge(st, merge);

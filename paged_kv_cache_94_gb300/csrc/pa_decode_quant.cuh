@@ -388,11 +388,12 @@ struct QuantMmaPolicy {
     // extra + 64*(BPI+j) (V). Tokens [lo, valid) of the item are attended,
     // those of block j only if bit j of mask is set (the block was loaded);
     // rem = ctx - (the item's first position), for the causal mask (NQ > 1).
-    // MASS: the scores of tokens [lo, valid) also go to srow[token][GQ].
-    template <bool MASS = false>
+    // MASS: the scores of tokens [lo, valid) also go to srow[token][GQ]. HOLE:
+    // tokens [0, valid) are attended but for the hole [lo, hole_end).
+    template <bool MASS = false, bool HOLE = false>
     __device__ static void compute(State &st, uint32_t kt, uint32_t extra, int lo, int valid,
                                    int rem, float scale_log2, uint32_t mask,
-                                   float *srow = nullptr)
+                                   float *srow = nullptr, int hole_end = 0)
     {
         const int lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
 
@@ -470,8 +471,8 @@ struct QuantMmaPolicy {
         for (int j = 0; j < BPI; ++j) {
             const int tl = 16 * j + gid, th = tl + 8;
             const bool in = (mask >> j) & 1u;
-            lo_ok[j] = in && tl >= lo && tl < valid;
-            hi_ok[j] = in && th >= lo && th < valid;
+            lo_ok[j] = in && (HOLE ? tl < lo || tl >= hole_end : tl >= lo) && tl < valid;
+            hi_ok[j] = in && (HOLE ? th < lo || th >= hole_end : th >= lo) && th < valid;
             const float f_lo = st.qexp * lds_f32(extra + 64 * j + 4 * gid) * scale_log2;
             const float f_hi = st.qexp * lds_f32(extra + 64 * j + 4 * (gid + 8)) * scale_log2;
 #pragma unroll

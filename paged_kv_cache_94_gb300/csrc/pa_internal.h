@@ -78,6 +78,9 @@ size_t cross_workspace_bytes(int d_h, int num_ctas);
 cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CrossArgs &a, cudaStream_t stream);
 
+// Decode over a window and the sequence's first tokens; NULL when not compiled.
+const DecodeKernel *find_window_kernel(int kind, int d_h, int group);
+
 // Rotary positions with the append (pa_rope.cu).
 struct RopeArgs {
     const void *q, *k, *v;

@@ -1,0 +1,56 @@
+"""Host-side checks of pa_window_decode: arguments refused before any CUDA call."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_kv_cache_94_gb300 as pa
+from paged_kv_cache_94_gb300 import build as pa_build
+
+FAKE = ctypes.c_void_p(256)  # never dereferenced: the calls return before any launch
+ODD = ctypes.c_void_p(258)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pa_build.build()
+    return pa.library()
+
+
+def _geom(**kw):
+    base = dict(num_blocks=100, n_h=32, n_kv=8, d_h=128, block_size=16, kv_dtype=0, reserved=0)
+    base.update(kw)
+    return pa.pa_geom(**base)
+
+
+def test_decode_argument_checks(lib):
+    def call(q=FAKE, kc=FAKE, ks=None, bt=FAKE, mb=16, ctx=FAKE, B=4, window=64, first=4, out=FAKE,
+             ws=FAKE, g=None, grid=0):
+        return lib.pa_window_decode(q, kc, FAKE, ks, ks, bt, mb, ctx, B, 0.1, window, first, out, ws,
+                                    1 << 20, g or _geom(), None, None, grid)
+    assert call(B=0) == 0
+    for kw in (dict(B=-1), dict(B=8193), dict(mb=0), dict(grid=-1), dict(window=-1), dict(first=-1)):
+        assert call(**kw) == -2, kw
+    assert call(mb=1 << 30) == -4
+    for kw in (dict(q=None), dict(kc=None), dict(bt=None), dict(ctx=None), dict(out=None)):
+        assert call(**kw) == -1, kw
+    assert call(ws=None) == -7
+    for kw in (dict(q=ODD), dict(kc=ODD), dict(out=ODD), dict(ws=ctypes.c_void_p(272))):
+        assert call(**kw) == -11, kw
+    assert call(ks=FAKE) == -2 and call(g=_geom(kv_dtype=1)) == -1
+    assert call(g=_geom(d_h=96)) == -4 and call(g=_geom(n_h=30)) == -2
+
+
+def test_decode_workspace_size(lib):
+    # counters, and a record for each CTA and unit
+    assert lib.pa_window_decode_workspace_size(_geom(), 4, 10) == 256 + (10 + 32) * 4 * 130 * 4
+    assert lib.pa_window_decode_workspace_size(_geom(d_h=96), 4, 10) == 0
+    assert lib.pa_window_decode_workspace_size(_geom(), -1, 10) == 0
+
+
+def test_decode_binding_refuses():
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_window_decode(q, kc, kc, i, i[0], 0.1, 4, 1)
