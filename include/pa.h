@@ -525,8 +525,42 @@ pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t 
                         int32_t *dev_status, void *stream);
 
 /*
- * pa_window_decode -- pa_decode over the last `window` tokens of each sequence and its
- * first n_first ones, which stay visible behind the window.
+ * pa_window_attention -- causal attention of any number of new tokens per sequence (a
+ * prompt, a chunk of one, a draft to verify) within a sliding window, and to the
+ * sequence's first tokens, which stay visible behind it.
+ *
+ * Tokens cu_q[b] <= t < cu_q[b + 1] are the last n = cu_q[b + 1] - cu_q[b] of sequence b's
+ * ctx_b, their K and V already in the cache: token cu_q[b] + i has position
+ * p = ctx_b - n + i and attends to
+ *     j <= p with j > p - window or j < n_first
+ * (window 0: all j <= p), softmax and scale as in pa_decode. A token with p < 0 gets a
+ * zero row.
+ *
+ *   window, n_first  >= 0 (PA_ERR_SHAPE)
+ * Block-table entries of blocks that no new token of the sequence sees are not read: those
+ * between the block of position n_first - 1 and the first one of the first new token's
+ * window may have been given back. K and V that a token does not see do not reach its row,
+ * whatever they hold; entries that are not finite make infinity or NaN of what sees them.
+ * Every other argument is pa_cross_attention's, the workspace's size
+ * pa_window_attention_workspace_size(geom, num_ctas). Accumulation and the weights'
+ * precision are pa_cross_attention's too; results do not depend on how the work was split
+ * beyond fp32 rounding, and are the same from call to call.
+ */
+pa_status pa_window_attention(const void *q, int64_t num_q, const int32_t *cu_q,
+                              const void *k_cache, const void *v_cache, const float *k_scale,
+                              const float *v_scale, const int32_t *block_tables,
+                              int32_t max_blocks_per_seq, const int32_t *context_lens,
+                              int32_t num_seqs, float scale, int32_t window, int32_t n_first,
+                              void *out, void *workspace, size_t workspace_bytes, pa_geom geom,
+                              int32_t *dev_status, void *stream, int32_t num_ctas);
+
+/* Workspace bytes pa_window_attention needs on the current device (it depends on the SM
+ * count when num_ctas is 0); 0 if an argument is invalid. */
+size_t pa_window_attention_workspace_size(pa_geom geom, int32_t num_ctas);
+
+/*
+ * pa_window_decode -- pa_window_attention of one new token per sequence: pa_decode over the
+ * last `window` tokens and the first n_first ones.
  *     attended: j < ctx_b with j >= ctx_b - window or j < n_first (window 0: all)
  * (pa_decode_opt's window has no first tokens: its n_sink are bf16 rows of positions inside
  * the window.) Block-table entries of blocks wholly between the two are not read: a

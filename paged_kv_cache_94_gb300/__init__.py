@@ -50,7 +50,8 @@ EXPORTED = ["pa_cache_write", "pa_decode_workspace_size", "pa_decode_workspace_i
             "pa_kv_read_probe", "pa_share_groups",
             "pa_decode_mass", "pa_decode_mass_workspace_size", "pa_evict_select",
             "pa_evict_compact", "pa_cross_attention", "pa_cross_workspace_size",
-            "pa_rope_write", "pa_window_decode", "pa_window_decode_workspace_size",
+            "pa_rope_write", "pa_window_attention", "pa_window_attention_workspace_size",
+            "pa_window_decode", "pa_window_decode_workspace_size",
             # host block manager (include/pa_alloc.h)
             "pa_allocator_create", "pa_allocator_destroy", "pa_allocator_allocate_prompt",
             "pa_allocator_allocate_private",
@@ -147,6 +148,11 @@ def _lib():
         lib.pa_rope_write.restype = ctypes.c_int
         lib.pa_rope_write.argtypes = [P, i64, P, i64, P, i64, i64, P, i32, P, P, i32, i32, f32, P, P,
                                       P, P, P, P, pa_geom, P, P]
+        lib.pa_window_attention_workspace_size.restype = sz
+        lib.pa_window_attention_workspace_size.argtypes = [pa_geom, i32]
+        lib.pa_window_attention.restype = ctypes.c_int
+        lib.pa_window_attention.argtypes = [P, i64, P, P, P, P, P, P, i32, P, i32, f32, i32, i32, P,
+                                            P, sz, pa_geom, P, P, i32]
         lib.pa_window_decode_workspace_size.restype = sz
         lib.pa_window_decode_workspace_size.argtypes = [pa_geom, i32, i32]
         lib.pa_window_decode.restype = ctypes.c_int
@@ -750,6 +756,15 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
     eviction kept; no causal mask) -> out of q's shape. Rows that no sequence has
     are left as they were (in a new out: not initialised). The pool (bf16, INT8,
     INT4), its scales and tables are pa_decode's."""
+    return _ragged("pa_cross_attention", q, cu_q, k_cache, v_cache, block_tables, context_lens,
+                   scale, (), out, k_scale, v_scale, workspace, dev_status, stream, num_ctas,
+                   prepare)
+
+
+def _ragged(what: str, q, cu_q, k_cache, v_cache, block_tables, context_lens, scale, mask: tuple,
+            out, k_scale, v_scale, workspace, dev_status, stream, num_ctas, prepare):
+    """pa_cross_attention, or with a mask (window, n_first) pa_window_attention. They share a
+    stream's workspace."""
     _need_cuda("q", q, torch.bfloat16)
     dev = q.device
     if q.dim() != 3 or block_tables.dim() != 2:
@@ -766,8 +781,9 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
     num_ctas = _int32("num_ctas", num_ctas)
     args = [q.data_ptr(), T, _take("cu_q", cu_q, torch.int32, dev), kp, vp, ks, vs,
             _take("block_tables", block_tables, torch.int32, dev), mb,
-            _take("context_lens", context_lens, torch.int32, dev), B, float(scale), None, None, 0,
-            g, _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
+            _take("context_lens", context_lens, torch.int32, dev), B, float(scale), *mask, None, None,
+            0, g, _opt("dev_status", dev_status, torch.int32, dev), None, num_ctas]
+    at = 12 + len(mask)
     with _on(dev, stream), _STREAM_LOCK:
         handle = _stream_handle(dev)
         owned = _Owned(dev) if prepare else None
@@ -785,11 +801,10 @@ def pa_cross_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tenso
             counters = (nbytes // (512 * (d + 2) * 4) * 4 + 255) // 256 * 256
             workspace = (owned.workspace(nbytes, counters) if prepare else
                          _stream_workspace("cross", nbytes, counters, dev, handle))
-        args[12] = _take("out", out, torch.bfloat16, dev)
-        args[13] = _take("workspace", workspace, workspace.dtype, dev)
-        args[14] = workspace.numel() * workspace.element_size()
-        return _issue(_lib().pa_cross_attention, args, 17, "pa_cross_attention", out, handle, stream,
-                      dev, owned)
+        args[at] = _take("out", out, torch.bfloat16, dev)
+        args[at + 1] = _take("workspace", workspace, workspace.dtype, dev)
+        args[at + 2] = workspace.numel() * workspace.element_size()
+        return _issue(getattr(_lib(), what), args, at + 5, what, out, handle, stream, dev, owned)
 
 
 def _rows_of(name: str, t: torch.Tensor, tokens: int, heads: int, d: int, device):
@@ -862,6 +877,28 @@ def pa_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
                       stream, dev, owned)
 
 
+def pa_window_attention(q: torch.Tensor, cu_q: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, scale: float, window: int = 0,
+                        n_first: int = 0, out: Optional[torch.Tensor] = None,
+                        k_scale: Optional[torch.Tensor] = None,
+                        v_scale: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        dev_status: Optional[torch.Tensor] = None, stream=None,
+                        num_ctas: int = 0, prepare: bool = False):
+    """Causal attention of new tokens within a sliding window, and to the first tokens of
+    their sequence: q [T, n_h, d_h] bf16, of which tokens cu_q[b] .. cu_q[b + 1] - 1 (cu_q
+    int32 [B + 1], on the device) are the last ones of sequence b's context_lens[b], whose
+    K and V are in the cache already (a prompt, a chunk of one, a draft to verify). A token
+    at position p sees j <= p with j > p - window or j < n_first (window 0: all j <= p).
+    -> out of q's shape. Blocks that no new token sees are not read: their table entries
+    may be anything. Rows that no sequence has are left as they were (in a new out: not
+    initialised). The pool (bf16, INT8, INT4), its scales and tables are pa_decode's."""
+    return _ragged("pa_window_attention", q, cu_q, k_cache, v_cache, block_tables, context_lens,
+                   scale, (_int32("window", window), _int32("n_first", n_first)), out, k_scale,
+                   v_scale, workspace, dev_status, stream, num_ctas, prepare)
+
+
 def pa_window_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                      window: int = 0, n_first: int = 0, out: Optional[torch.Tensor] = None,
@@ -871,7 +908,8 @@ def pa_window_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      dev_status: Optional[torch.Tensor] = None, stream=None, num_ctas: int = 0,
                      prepare: bool = False):
     """pa_decode over the last `window` tokens of each sequence (0: all) and its first
-    n_first ones. q [B, n_h, d_h] bf16 -> out of q's shape. Blocks wholly between the two
+    n_first ones: pa_window_attention of one new token per sequence. q [B, n_h, d_h] bf16
+    -> out of q's shape. Blocks wholly between the two
     are not read: their table entries may be anything. Everything else as pa_decode
     without its options."""
     _need_cuda("q", q, torch.bfloat16)

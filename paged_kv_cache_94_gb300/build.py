@@ -43,6 +43,7 @@ SOURCES = [
     "pa_decode_window_int8.cu",
     "pa_decode_window_int4.cu",
     "pa_cross.cu",
+    "pa_window.cu",
     "pa_rope.cu",
     "pa_mass.cu",
     "pa_evict.cu",

@@ -497,6 +497,79 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Cross attention, or (wa not NULL) window attention.
+pa_status cross_impl(const void *q, int64_t num_q, const int32_t *cu_q, const void *k_cache,
+                     const void *v_cache, const float *k_scale, const float *v_scale,
+                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                     const int32_t *context_lens, int32_t num_seqs, float scale, void *out,
+                     void *workspace, size_t workspace_bytes, pa_geom geom, int32_t *dev_status,
+                     void *stream, int32_t num_ctas, const WindowArgs *wa)
+{
+    pa_status st = check_geom(geom);
+    if (st != PA_OK)
+        return st;
+    if (wa && (wa->window < 0 || wa->n_first < 0))
+        return PA_ERR_SHAPE;
+    if (num_q < 0 || num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq <= 0 ||
+        num_ctas < 0 || num_ctas > kMaxCrossCtas)
+        return PA_ERR_SHAPE;
+    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31) ||
+        num_q >= (int64_t(1) << 31) / geom.n_h)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_q == 0)
+        return PA_OK;
+    if (!q || !cu_q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||
+        !workspace)
+        return !workspace ? PA_ERR_WORKSPACE : PA_ERR_NULL;
+    const bool i8 = geom.kv_dtype != PA_KV_BF16; // INT8 or INT4: fp32 scales
+    if (i8 && (!k_scale || !v_scale))
+        return PA_ERR_NULL;
+    if (!i8 && (k_scale || v_scale))
+        return PA_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
+        return PA_ERR_ALIGNMENT;
+    int dev, sms;
+    if ((st = current_device(dev, sms)) != PA_OK)
+        return st;
+    const int grid = num_ctas > 0 ? num_ctas : sms;
+    if (workspace_bytes < pa::cross_workspace_bytes(geom.d_h, grid))
+        return PA_ERR_WORKSPACE;
+    CUtensorMap tq, tk, tv;
+    if ((st = encode_queries(tq, q, geom, num_q)) != PA_OK ||
+        (st = encode_pool(tk, k_cache, geom)) != PA_OK ||
+        (st = encode_pool(tv, v_cache, geom)) != PA_OK)
+        return st;
+    pa::CrossArgs a;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cu_q = cu_q;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.out = out;
+    a.workspace = workspace;
+    a.dev_status = dev_status;
+    a.num_q = num_q;
+    a.num_blocks = geom.num_blocks;
+    a.num_seqs = num_seqs;
+    a.n_kv = geom.n_kv;
+    a.g = group_of(geom);
+    a.d_h = geom.d_h;
+    a.kind = geom.kv_dtype;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_ctas = grid;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.window = wa ? wa->window : 0;
+    a.n_first = wa ? wa->n_first : 0;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        wa ? pa::launch_window(tq, tk, tv, a, cs) : pa::launch_cross(tq, tk, tv, a, cs);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 } // namespace
 
 namespace pa {
@@ -917,64 +990,29 @@ pa_status pa_cross_attention(const void *q, int64_t num_q, const int32_t *cu_q,
                              void *stream, int32_t num_ctas)
 {
     const NvtxRange range("pa_cross_attention");
-    pa_status st = check_geom(geom);
-    if (st != PA_OK)
-        return st;
-    if (num_q < 0 || num_seqs < 0 || num_seqs > kMaxSeqs || max_blocks_per_seq <= 0 ||
-        num_ctas < 0 || num_ctas > kMaxCrossCtas)
-        return PA_ERR_SHAPE;
-    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t(1) << 31) ||
-        num_q >= (int64_t(1) << 31) / geom.n_h)
-        return PA_ERR_UNSUPPORTED;
-    if (num_seqs == 0 || num_q == 0)
-        return PA_OK;
-    if (!q || !cu_q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||
-        !workspace)
-        return !workspace ? PA_ERR_WORKSPACE : PA_ERR_NULL;
-    const bool i8 = geom.kv_dtype != PA_KV_BF16; // INT8 or INT4: fp32 scales
-    if (i8 && (!k_scale || !v_scale))
-        return PA_ERR_NULL;
-    if (!i8 && (k_scale || v_scale))
-        return PA_ERR_SHAPE;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-        !aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
-        !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
-        return PA_ERR_ALIGNMENT;
-    int dev, sms;
-    if ((st = current_device(dev, sms)) != PA_OK)
-        return st;
-    const int grid = num_ctas > 0 ? num_ctas : sms;
-    if (workspace_bytes < pa::cross_workspace_bytes(geom.d_h, grid))
-        return PA_ERR_WORKSPACE;
-    CUtensorMap tq, tk, tv;
-    if ((st = encode_queries(tq, q, geom, num_q)) != PA_OK ||
-        (st = encode_pool(tk, k_cache, geom)) != PA_OK ||
-        (st = encode_pool(tv, v_cache, geom)) != PA_OK)
-        return st;
-    pa::CrossArgs a;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.cu_q = cu_q;
-    a.block_tables = block_tables;
-    a.context_lens = context_lens;
-    a.out = out;
-    a.workspace = workspace;
-    a.dev_status = dev_status;
-    a.num_q = num_q;
-    a.num_blocks = geom.num_blocks;
-    a.num_seqs = num_seqs;
-    a.n_kv = geom.n_kv;
-    a.g = group_of(geom);
-    a.d_h = geom.d_h;
-    a.kind = geom.kv_dtype;
-    a.max_blocks = max_blocks_per_seq;
-    a.num_ctas = grid;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    return pa::launch_cross(tq, tk, tv, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    return cross_impl(q, num_q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                      max_blocks_per_seq, context_lens, num_seqs, scale, out, workspace,
+                      workspace_bytes, geom, dev_status, stream, num_ctas, nullptr);
+}
+
+size_t pa_window_attention_workspace_size(pa_geom geom, int32_t num_ctas)
+{
+    return pa_cross_workspace_size(geom, num_ctas);
+}
+
+pa_status pa_window_attention(const void *q, int64_t num_q, const int32_t *cu_q,
+                              const void *k_cache, const void *v_cache, const float *k_scale,
+                              const float *v_scale, const int32_t *block_tables,
+                              int32_t max_blocks_per_seq, const int32_t *context_lens,
+                              int32_t num_seqs, float scale, int32_t window, int32_t n_first,
+                              void *out, void *workspace, size_t workspace_bytes, pa_geom geom,
+                              int32_t *dev_status, void *stream, int32_t num_ctas)
+{
+    const NvtxRange range("pa_window_attention");
+    const WindowArgs wa = {window, n_first};
+    return cross_impl(q, num_q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                      max_blocks_per_seq, context_lens, num_seqs, scale, out, workspace,
+                      workspace_bytes, geom, dev_status, stream, num_ctas, &wa);
 }
 
 pa_status pa_evict_select(const float *mass, int64_t max_tokens, const int32_t *context_lens,

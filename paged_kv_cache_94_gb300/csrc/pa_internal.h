@@ -63,7 +63,7 @@ cudaError_t launch_mass(const float *scores, const float2 *ml, const int32_t *co
                         const float *mass, float *mass_out, int num_seqs, int n_kv, int g,
                         int max_blocks, int sms, cudaStream_t stream);
 
-// Cross attention (pa_cross.cu).
+// Cross attention (pa_cross.cu) and window attention (pa_window.cu).
 struct CrossArgs {
     const void *k_cache, *v_cache;
     const float *k_scale, *v_scale;
@@ -73,10 +73,13 @@ struct CrossArgs {
     int64_t num_q, num_blocks;
     int num_seqs, n_kv, g, d_h, kind, max_blocks, num_ctas;
     float scale_log2;
+    int window, n_first;
 };
 size_t cross_workspace_bytes(int d_h, int num_ctas);
 cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CrossArgs &a, cudaStream_t stream);
+cudaError_t launch_window(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const CrossArgs &a, cudaStream_t stream);
 
 // Decode over a window and the sequence's first tokens; NULL when not compiled.
 const DecodeKernel *find_window_kernel(int kind, int d_h, int group);

@@ -1,4 +1,4 @@
-"""Host-side checks of pa_window_decode: arguments refused before any CUDA call."""
+"""Host-side checks of pa_window_attention and pa_window_decode: arguments refused before any CUDA call."""
 import ctypes
 
 import pytest
@@ -54,3 +54,36 @@ def test_decode_binding_refuses():
     i = torch.zeros(1, 1, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         pa.pa_window_decode(q, kc, kc, i, i[0], 0.1, 4, 1)
+
+
+def test_attention_argument_checks(lib):
+    def call(q=FAKE, T=64, cu=FAKE, kc=FAKE, ks=None, bt=FAKE, mb=16, ctx=FAKE, B=4, window=64,
+             first=4, out=FAKE, ws=FAKE, g=None, grid=0):
+        return lib.pa_window_attention(q, T, cu, kc, FAKE, ks, ks, bt, mb, ctx, B, 0.1, window, first,
+                                       out, ws, 1 << 20, g or _geom(), None, None, grid)
+    assert call(B=0) == 0 and call(T=0) == 0
+    for kw in (dict(T=-1), dict(B=-1), dict(B=8193), dict(mb=0), dict(grid=-1), dict(grid=8193),
+               dict(window=-1), dict(first=-1)):
+        assert call(**kw) == -2, kw
+    assert call(T=1 << 26) == -4 and call(mb=1 << 30) == -4
+    for kw in (dict(q=None), dict(cu=None), dict(kc=None), dict(bt=None), dict(ctx=None),
+               dict(out=None)):
+        assert call(**kw) == -1, kw
+    assert call(ws=None) == -7
+    for kw in (dict(q=ODD), dict(cu=ODD), dict(kc=ODD), dict(out=ODD), dict(bt=ODD),
+               dict(ctx=ODD), dict(ws=ctypes.c_void_p(272))):
+        assert call(**kw) == -11, kw
+    assert call(ks=FAKE) == -2 and call(g=_geom(kv_dtype=1)) == -1
+    assert call(g=_geom(d_h=96)) == -4 and call(g=_geom(n_h=30)) == -2
+
+
+def test_attention_workspace_size_and_binding(lib):
+    assert lib.pa_window_attention_workspace_size(_geom(), 100) == 512 + 100 * 2 * 256 * 130 * 4
+    assert lib.pa_window_attention_workspace_size(_geom(d_h=96), 4) == 0
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_window_attention(q, torch.zeros(2, dtype=torch.int32), kc, kc, i, i[0], 0.1, 4, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        pa.pa_window_attention(q, torch.zeros(2, dtype=torch.int32), kc, kc, i, i[0], 0.1, 1 << 40)
