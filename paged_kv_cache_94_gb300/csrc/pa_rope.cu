@@ -12,13 +12,17 @@
 //
 // What bounds it: memory for prompts (each row read once and written once), latency for a
 // decode step. A thread takes 16 values of a row, both halves of its eight pairs, as two
-// 16-byte pieces; a CTA some tokens, whose sines and cosines it works out once for all heads
-// while the first rows are on their way.
+// 16-byte loads, the same ones of every row that it comes to; a CTA some tokens, whose sines
+// and cosines it works out once for all heads while the first rows are on their way.
+//
+// Measured on a GB300: 8192 tokens of 32 + 8 heads of 128 into a bf16 pool 39 us, 5170 GB/s,
+// 0.76 of the measured copy rate (56 with rows found by division and 98 registers, two CTAs
+// per SM); into an INT8 pool 43. 4111 tokens of 16 + 16 heads of 64 into an INT8 pool 13.5 us
+// (21.5 where one near half had all eight values divided, 18.7 with a division each). A step
+// of 64 tokens 2.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <algorithm>
 
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
@@ -27,8 +31,6 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 64;
-constexpr int kMaxTokens = 32; // of one CTA
 
 struct RopeParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -44,9 +46,9 @@ struct RopeParams {
     int64_t num_tokens, num_slots;
     float amplitude;
     int32_t n_axes, pairs, n_h, n_kv;
-    int32_t tokens; // of one CTA
     int32_t rows;   // of a token: n_h + 2 n_kv
-    int32_t adjacent;
+    int32_t tokens; // of one CTA
+    int32_t round_rows, round_tokens; // how far a thread's row moves from round to round
 };
 
 // cos and sin of position * freq, freq in radians per position.
@@ -90,120 +92,156 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8])
                       pack_bf16x2(x[6], x[7]));
 }
 
-// Codes of eight values (the quantiser of pa_cache_write).
+// Codes of eight values (the quantiser of pa_cache_write): the correctly rounded quotient
+// x / scale, rounded to an integer, half to even. x times the reciprocal is off by less than
+// 2^-14 (two roundings of up to 128), so where it is at least that far from a half both round
+// to the same integer; the rest is divided, value by value: few, but half the largest value of
+// a row, which bf16 rows often have, is 63.5 or 3.5 itself. Adding 1.5 * 2^23 rounds a small
+// number to an integer, which the sum's low bits hold in two's complement (rint and the
+// conversion run at an eighth of the rate). inv: 1 / scale, 0 where all codes are 0.
 template <int KIND>
-__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float scale)
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float scale, float inv)
 {
-    uint32_t w[2] = {0, 0};
+    constexpr float top = KIND == 1 ? 127.f : 7.f, kRound = 12582912.f;
+    float c[8];
+    uint32_t near = inv < 1e30f ? 0u : 0xffu; // (a scale near 0: all)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float c = 0.f;
-        if (scale != 0.f) {
-            c = rintf(__fdiv_rn(x[i], scale));
-            c = KIND == 1 ? fminf(fmaxf(c, -128.f), 127.f) : fminf(fmaxf(c, -8.f), 7.f);
-        }
-        if constexpr (KIND == 1)
-            w[i / 4] |= (uint32_t)(uint8_t)(int8_t)(int)c << (8 * (i % 4));
-        else
-            w[0] |= ((uint32_t)(int)c & 0xFu) << (4 * i);
+        const float r = x[i] * inv;
+        c[i] = r + kRound;
+        if (!(fabsf(r - (c[i] - kRound)) < 0.5f - 6.1035156e-5f)) // (or not a number)
+            near |= 1u << i;
     }
-    return make_uint2(w[0], w[1]);
+#pragma unroll 1
+    for (; near; near &= near - 1) {
+        const int i = __ffs(near) - 1;
+        float r = 0.f; // (x and c stay in registers: no index that is not a constant)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            r = e == i ? x[e] : r;
+        r = scale != 0.f ? fminf(fmaxf(rintf(__fdiv_rn(r, scale)), -top - 1.f), top) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            c[e] = e == i ? r + kRound : c[e];
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = __float_as_uint(c[i]);
+    if constexpr (KIND == 1)
+        return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040),
+                                      __byte_perm(w[2], w[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(w[4], w[5], 0x0040),
+                                      __byte_perm(w[6], w[7], 0x0040), 0x5410));
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        n |= (w[i] & 0xfu) << (4 * i);
+    return make_uint2(n, 0);
 }
 
-// KIND: 0 bf16, 1 INT8, 2 INT4; U: pieces of a thread whose loads are in flight together
-template <int D, int KIND, int U>
-__global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeParams p)
+// KIND: 0 bf16, 1 INT8, 2 INT4; ADJ: pairs are adjacent values; U: pieces of a thread whose
+// loads are in flight together
+template <int D, int KIND, bool ADJ, int U>
+__global__ void __launch_bounds__(kThreads, U == 1 ? 1 : 4) rope_write_kernel(const RopeParams p)
 {
     // a decode launched next on the stream may be scheduled now; it waits for
     // this grid to complete before reading the cache
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int PPR = D / 16; // pieces of a row
-    __shared__ float2 turns[kMaxTokens * kMaxPairs];
+    constexpr int PPR = D / 16, STEP = kThreads / PPR; // pieces of a row, rows of a round
+    extern __shared__ __align__(16) float2 turns[];    // [tokens][pairs]
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int tokens = (int)min((int64_t)p.tokens, p.num_tokens - t0);
-    const int per_token = p.rows * PPR, pieces = tokens * per_token;
-    bool made = false;
-    for (int i0 = blockIdx.y * (kThreads * U) + tid; i0 - tid < pieces;
-         i0 += gridDim.y * (kThreads * U)) {
+    // this thread's piece of its rows: values from .. from + 7 and from + gap .. from + gap + 7
+    const int c = tid % PPR;
+    const bool turns_it = ADJ ? 16 * c < 2 * p.pairs : 8 * c < p.pairs;
+    const int from = !ADJ && turns_it ? 8 * c : 16 * c, gap = !ADJ && turns_it ? p.pairs : 8;
+    const float4 *cs = reinterpret_cast<const float4 *>(turns + (ADJ ? 8 * c : from));
+    // row `row` of token `tok`, STEP rows further on from round to round
+    int tok = 0, row = blockIdx.y * (STEP * U) + tid / PPR;
+    if (row >= p.rows) {
+        tok = row / p.rows;
+        row -= tok * p.rows;
+    }
+    const int rounds = gridDim.y > 1 ? 1 : (tokens * p.rows + STEP * U - 1) / (STEP * U);
+    for (int round = 0; round < rounds; ++round) {
         uint4 a[U], b[U];
-        int tok[U], row[U], from[U], step[U]; // a piece's values: from .. + 7, from + step ..
         int64_t slot[U];
-        bool live[U];
+        int at_tok[U], at_row[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kThreads;
-            live[u] = i < pieces;
-            tok[u] = live[u] ? i / per_token : 0;
-            const int r = live[u] ? i - tok[u] * per_token : 0, c = r % PPR;
-            row[u] = r / PPR;
-            const bool halves = !p.adjacent && 8 * c < p.pairs;
-            from[u] = halves ? 8 * c : 16 * c;
-            step[u] = halves ? p.pairs : 8;
-            const int h = row[u];
-            const int64_t t = t0 + tok[u];
-            const __nv_bfloat16 *src =
-                h < p.n_h            ? p.q + t * p.q_stride + h * D
-                : h < p.n_h + p.n_kv ? p.k + t * p.k_stride + (h - p.n_h) * D
-                                     : p.v + t * p.v_stride + (h - p.n_h - p.n_kv) * D;
+            const bool live = tok < tokens;
+            at_tok[u] = live ? tok : -1;
+            at_row[u] = row;
+            const int64_t t = t0 + tok;
+            const bool is_q = row < p.n_h, is_k = row < p.n_h + p.n_kv;
+            const __nv_bfloat16 *src = is_q ? p.q : is_k ? p.k : p.v;
+            const int64_t stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
+            const int h = row - (is_q ? 0 : is_k ? p.n_h : p.n_h + p.n_kv);
+            src += t * stride + h * D + from;
             a[u] = b[u] = make_uint4(0, 0, 0, 0);
-            slot[u] = live[u] && h >= p.n_h ? p.slots[t] : -1;
-            if (live[u]) {
-                a[u] = *reinterpret_cast<const uint4 *>(src + from[u]);
-                b[u] = *reinterpret_cast<const uint4 *>(src + from[u] + step[u]);
+            slot[u] = -1;
+            if (live) {
+                a[u] = *reinterpret_cast<const uint4 *>(src);
+                b[u] = *reinterpret_cast<const uint4 *>(src + gap);
+                if (!is_q)
+                    slot[u] = p.slots[t];
+            }
+            row += p.round_rows;
+            tok += p.round_tokens;
+            if (row >= p.rows) {
+                row -= p.rows;
+                ++tok;
             }
         }
-        if (!made) {
-            made = true;
+        if (round == 0) {
             for (int j = tid; j < tokens * p.pairs; j += kThreads) {
                 const int t = j / p.pairs, i = j - t * p.pairs;
                 const int axis = p.axis ? p.axis[i] : 0;
-                float2 cs = make_float2(1.f, 0.f); // (an axis that is not there turns nothing)
+                float2 w = make_float2(1.f, 0.f); // (an axis that is not there turns nothing)
                 if (axis >= 0 && axis < p.n_axes)
-                    cs = turn_of(p.positions[axis * p.num_tokens + t0 + t], p.inv_freq[i],
-                                 p.amplitude);
+                    w = turn_of(p.positions[axis * p.num_tokens + t0 + t], p.inv_freq[i],
+                                p.amplitude);
                 else if (p.dev_status)
                     atomicOr(p.dev_status, PA_DEV_BAD_CONTEXT_BIT);
-                turns[t * kMaxPairs + i] = cs;
+                turns[j] = w;
             }
             __syncthreads();
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const bool live = at_tok[u] >= 0;
+            const bool is_q = at_row[u] < p.n_h, is_v = at_row[u] >= p.n_h + p.n_kv;
             float x[8], y[8];
-            unpack(a[u], x);
-            unpack(b[u], y);
-            const bool is_v = row[u] >= p.n_h + p.n_kv;
-            const int pair = p.adjacent ? from[u] / 2 : from[u];
-            if (!is_v && (p.adjacent ? from[u] < 2 * p.pairs
-                                     : step[u] == p.pairs && from[u] < p.pairs)) {
-                const float4 *cs =
-                    reinterpret_cast<const float4 *>(turns + tok[u] * kMaxPairs + pair);
+            if (KIND != 0 || !is_v) {
+                unpack(a[u], x);
+                unpack(b[u], y);
+            }
+            if (live && turns_it && !is_v) {
+                const float4 *w4 = cs + at_tok[u] * (p.pairs / 2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { // two pairs at a time
-                    const float4 w = cs[e];
-                    if (p.adjacent) {
-                        float *z = e < 2 ? x + 4 * e : y + 4 * (e - 2);
-                        const float a0 = z[0], b0 = z[1], a1 = z[2], b1 = z[3];
-                        z[0] = a0 * w.x - b0 * w.y;
-                        z[1] = b0 * w.x + a0 * w.y;
-                        z[2] = a1 * w.z - b1 * w.w;
-                        z[3] = b1 * w.z + a1 * w.w;
-                    } else {
-                        const float a0 = x[2 * e], b0 = y[2 * e], a1 = x[2 * e + 1],
-                                    b1 = y[2 * e + 1];
-                        x[2 * e] = a0 * w.x - b0 * w.y;
-                        y[2 * e] = b0 * w.x + a0 * w.y;
-                        x[2 * e + 1] = a1 * w.z - b1 * w.w;
-                        y[2 * e + 1] = b1 * w.z + a1 * w.w;
-                    }
+                    const float4 w = w4[e];
+                    float *m = ADJ ? (e < 2 ? x + 4 * e : y + 4 * (e - 2)) : x + 2 * e;
+                    float *n = ADJ ? m + 1 : y + 2 * e;
+                    constexpr int next = ADJ ? 2 : 1;
+                    const float a0 = m[0], b0 = n[0], a1 = m[next], b1 = n[next];
+                    m[0] = a0 * w.x - b0 * w.y;
+                    n[0] = b0 * w.x + a0 * w.y;
+                    m[next] = a1 * w.z - b1 * w.w;
+                    n[next] = b1 * w.z + a1 * w.w;
                 }
             }
-            const int64_t t = t0 + tok[u];
-            if (row[u] < p.n_h && live[u]) {
-                __nv_bfloat16 *dst = p.out + (t * p.n_h + row[u]) * D + from[u];
-                *reinterpret_cast<uint4 *>(dst) = pack(x);
-                *reinterpret_cast<uint4 *>(dst + step[u]) = pack(y);
+            if ((KIND == 0 || is_q) && !is_v) {
+                a[u] = pack(x);
+                b[u] = pack(y);
+            }
+            if (live && is_q) {
+                __nv_bfloat16 *dst =
+                    p.out + ((t0 + at_tok[u]) * p.n_h + at_row[u]) * D + from;
+                *reinterpret_cast<uint4 *>(dst) = a[u];
+                *reinterpret_cast<uint4 *>(dst + gap) = b[u];
             }
             float scale = 0.f;
             if constexpr (KIND != 0) { // (all lanes of a warp take part)
@@ -216,11 +254,11 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeParams p
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 scale = __fdiv_rn(m, KIND == 1 ? 127.f : 7.f);
             }
-            if (row[u] < p.n_h || !live[u])
+            if (is_q || !live)
                 continue;
             const int64_t s = slot[u];
-            const int h = row[u] - p.n_h - (is_v ? p.n_kv : 0);
-            const bool lead = from[u] == 0;
+            const int h = at_row[u] - p.n_h - (is_v ? p.n_kv : 0);
+            const bool lead = c == 0;
             if (s < 0 || s >= p.num_slots) {
                 if (s >= 0 && lead && h == 0 && p.dev_status)
                     atomicOr(p.dev_status, PA_DEV_BAD_SLOT_BIT);
@@ -229,19 +267,20 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeParams p
             const int64_t dst_row = ((s >> 4) * p.n_kv + h) * 16 + (s & 15);
             void *pool = is_v ? p.v_cache : p.k_cache;
             if constexpr (KIND == 0) {
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(pool) + dst_row * D + from[u];
-                *reinterpret_cast<uint4 *>(dst) = is_v ? a[u] : pack(x);
-                *reinterpret_cast<uint4 *>(dst + step[u]) = is_v ? b[u] : pack(y);
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(pool) + dst_row * D + from;
+                *reinterpret_cast<uint4 *>(dst) = a[u];
+                *reinterpret_cast<uint4 *>(dst + gap) = b[u];
             } else {
-                const uint2 cx = codes_of<KIND>(x, scale), cy = codes_of<KIND>(y, scale);
+                const float inv = scale != 0.f ? __frcp_rn(scale) : 0.f;
+                const uint2 cx = codes_of<KIND>(x, scale, inv), cy = codes_of<KIND>(y, scale, inv);
                 if constexpr (KIND == 1) {
-                    int8_t *dst = static_cast<int8_t *>(pool) + dst_row * D + from[u];
+                    int8_t *dst = static_cast<int8_t *>(pool) + dst_row * D + from;
                     *reinterpret_cast<uint2 *>(dst) = cx;
-                    *reinterpret_cast<uint2 *>(dst + step[u]) = cy;
+                    *reinterpret_cast<uint2 *>(dst + gap) = cy;
                 } else {
-                    uint8_t *dst = static_cast<uint8_t *>(pool) + (dst_row * D + from[u]) / 2;
+                    uint8_t *dst = static_cast<uint8_t *>(pool) + (dst_row * D + from) / 2;
                     *reinterpret_cast<uint32_t *>(dst) = cx.x;
-                    *reinterpret_cast<uint32_t *>(dst + step[u] / 2) = cy.x;
+                    *reinterpret_cast<uint32_t *>(dst + gap / 2) = cy.x;
                 }
                 if (lead)
                     (is_v ? p.v_scale : p.k_scale)[dst_row] = scale;
@@ -250,27 +289,47 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeParams p
     }
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool ADJ>
 cudaError_t launch_of(const RopeParams &p, int sms, cudaStream_t stream)
 {
-    using std::max;
-    using std::min;
+    constexpr int STEP = kThreads / (D / 16);
     RopeParams r = p;
-    const int per_token = p.rows * (D / 16);
-    const int64_t all = p.num_tokens * per_token;
-    const int64_t few = (int64_t)sms * 2 * kThreads; // pieces that go one to a thread
-    if (all <= few) {
+    const int64_t rounds = (p.rows + STEP - 1) / STEP; // of one token alone
+    if (p.num_tokens * rounds <= 2 * sms) {            // few: a round to a CTA
         r.tokens = 1;
-        const dim3 grid((unsigned)p.num_tokens, (unsigned)((per_token + kThreads - 1) / kThreads));
-        rope_write_kernel<D, KIND, 1><<<grid, kThreads, 0, stream>>>(r);
+        r.round_rows = 0;
+        r.round_tokens = 1; // the one round is the last
+        rope_write_kernel<D, KIND, ADJ, 1>
+            <<<dim3((unsigned)p.num_tokens, (unsigned)rounds), kThreads,
+               p.pairs * sizeof(float2), stream>>>(r);
     } else {
-        r.tokens = max(1, min(kMaxTokens, 4 * kThreads / per_token));
+        // Tokens of a CTA, up to a sine and cosine to a thread: the fewest rounds, and one for
+        // the CTA's start, over all waves of four CTAs to an SM.
+        int64_t best = INT64_MAX;
+        for (int t = 1; t <= kThreads / p.pairs; ++t) {
+            const int64_t waves = (p.num_tokens + (int64_t)t * 4 * sms - 1) / ((int64_t)t * 4 * sms);
+            const int64_t cost = waves * (((int64_t)t * p.rows + 2 * STEP - 1) / (2 * STEP) + 1);
+            if (cost < best) {
+                best = cost;
+                r.tokens = t;
+            }
+        }
+        r.round_rows = STEP % p.rows;
+        r.round_tokens = STEP / p.rows;
         const int64_t blocks = (p.num_tokens + r.tokens - 1) / r.tokens;
         if (blocks > 0x7fffffff)
             return cudaErrorInvalidValue;
-        rope_write_kernel<D, KIND, 4><<<(unsigned)blocks, kThreads, 0, stream>>>(r);
+        rope_write_kernel<D, KIND, ADJ, 2>
+            <<<(unsigned)blocks, kThreads, r.tokens * p.pairs * sizeof(float2), stream>>>(r);
     }
     return cudaGetLastError();
+}
+
+template <int D, int KIND>
+cudaError_t launch_of(const RopeParams &p, bool adjacent, int sms, cudaStream_t stream)
+{
+    return adjacent ? launch_of<D, KIND, true>(p, sms, stream)
+                    : launch_of<D, KIND, false>(p, sms, stream);
 }
 
 } // namespace
@@ -301,16 +360,16 @@ cudaError_t launch_rope_write(const RopeArgs &a, int sms, cudaStream_t stream)
     p.pairs = a.pairs;
     p.n_h = a.n_h;
     p.n_kv = a.n_kv;
-    p.tokens = 1;
     p.rows = a.n_h + 2 * a.n_kv;
-    p.adjacent = a.adjacent;
+    p.tokens = 1;
+    p.round_rows = p.round_tokens = 0;
     if (a.d_h == 128)
-        return a.kind == 0   ? launch_of<128, 0>(p, sms, stream)
-               : a.kind == 1 ? launch_of<128, 1>(p, sms, stream)
-                             : launch_of<128, 2>(p, sms, stream);
-    return a.kind == 0   ? launch_of<64, 0>(p, sms, stream)
-           : a.kind == 1 ? launch_of<64, 1>(p, sms, stream)
-                         : launch_of<64, 2>(p, sms, stream);
+        return a.kind == 0   ? launch_of<128, 0>(p, a.adjacent != 0, sms, stream)
+               : a.kind == 1 ? launch_of<128, 1>(p, a.adjacent != 0, sms, stream)
+                             : launch_of<128, 2>(p, a.adjacent != 0, sms, stream);
+    return a.kind == 0   ? launch_of<64, 0>(p, a.adjacent != 0, sms, stream)
+           : a.kind == 1 ? launch_of<64, 1>(p, a.adjacent != 0, sms, stream)
+                         : launch_of<64, 2>(p, a.adjacent != 0, sms, stream);
 }
 
 } // namespace pa
