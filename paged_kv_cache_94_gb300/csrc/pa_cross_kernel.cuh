@@ -555,17 +555,22 @@ __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity)
 // Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n)
 {
-    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    uint32_t above;
+    asm("shl.b32 %0, %1, %2;" : "=r"(above) : "r"(0xffffffffu), "r"(max(n, 0))); // (0 from 32 on)
+    return ~above;
+}
+
+// WIN: the first virtual position of the window of a token at virtual position p.
+__device__ __forceinline__ int window_from(const CrossParams &q, int p)
+{
+    return q.window ? max(p + 1 - q.window, 0) : 0;
 }
 
 // WIN: the 32 keys from virtual position k on that a token at virtual position p sees.
 __device__ __forceinline__ uint32_t seen_keys(const CrossParams &q, int p, int k)
 {
-    const uint32_t past = bits_below(p + 1 - k);
-    if (q.window == 0)
-        return past;
-    return past & (bits_below(q.n_first - k) |
-                   ~bits_below((int)max((int64_t)p + 1 - q.window - k, (int64_t)-1)));
+    return bits_below(p + 1 - k) &
+           (bits_below(q.n_first - k) | ~bits_below(window_from(q, p) - k));
 }
 
 // One step of the online softmax over 64 keys of an INT8/INT4 tile, of a warp's 32 rows. A
@@ -909,6 +914,10 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // WIN: the virtual position of this thread's row (INT8/INT4: see quad_step)
             const int p0 = WIN ? g.p0() : 0;
             const int pos = p0 + ((two ? half * kRows + row : row) >> p.log2_g);
+            // ... and those of this warp's first and last row
+            const int warp_row = (two ? half * kRows : 0) + (row & ~31);
+            const int pos_first = p0 + (warp_row >> p.log2_g),
+                      pos_last = p0 + ((warp_row + 31) >> p.log2_g);
             bool poison = false; // this thread's row has seen a V entry that is not finite
             uint32_t *poisons = reinterpret_cast<uint32_t *>(smem + L::kOffPoison) + tid;
             uint32_t n_s = half ? n_b[1] : n_b[0];
@@ -922,43 +931,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     scales + ((n_tile + (uint32_t)(j - g.j0)) % kScaleRing) * 2 * kRows;
                 const int tail = ctx % kBlockTokens;
                 const bool masked = WIN && g.masked(p, j);
-                if (L::kCheck && masked) {
-                    // The rows of V that are not finite were zeroed in the tile (see there);
-                    // what this row sees of them joins its output at the end.
-                    const uint32_t fill = 2 * (n_tile + (uint32_t)(j - g.j0)) + 1;
-                    const volatile uint32_t *odd =
-                        reinterpret_cast<const uint32_t *>(smem + L::kOffOdd) + fill % SLOTS * 4;
-                    if (wait(kv_full + 8 * (fill % SLOTS), fill / SLOTS))
-#pragma unroll 1
-                        for (int w = 0; w < kRows / 32; ++w) {
-                            uint32_t rows = odd[w];
-                            if (rows == 0)
-                                continue;
-                            rows &= seen_keys(p, pos, j * kRows + 32 * w);
-#pragma unroll 1
-                            for (; rows; rows &= rows - 1) {
-                                const int key = j * kRows + 32 * w + __ffs(rows) - 1;
-                                int blk = key / kBlockTokens;
-                                blk += blk < g.span.kept ? 0 : g.span.skip;
-                                const int64_t at =
-                                    (int64_t)__ldg(p.block_tables +
-                                                   (int64_t)walk.at.b * p.max_blocks + blk) *
-                                        p.n_kv + g.kvh;
-                                const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                                    static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                                    (at * kBlockTokens + key % kBlockTokens) * D);
-                                if (!poison)
-                                    for (int c = 0; c < D / 32; ++c)
-                                        poisons[c * kUnitRows] = 0;
-                                poison = true;
-#pragma unroll 1
-                                for (int d = 0; d < D; ++d)
-                                    if ((v[d / 2] >> (d % 2 * 16) & 0x7f80u) == 0x7f80u)
-                                        poisons[d / 32 * kUnitRows] |= 1u << (d % 32);
-                            }
-                        }
-                    __syncwarp();
-                }
                 if (!WIN && KIND == 0 && tail && j == walk.s.tiles - 1) {
                     // V rows behind the context may hold anything, and 0 * NaN is NaN: zero
                     // them before this half's products (both halves write the same zeros)
@@ -980,11 +952,31 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 for (int part = 0; part < 2; ++part) {
                     const int c0 = part * kPart;
                     const bool first = part == 0 && j == j_first;
-                    if constexpr (KIND != 0) {
+                    // WIN: what this warp's rows see of the step: nothing, all, or some of it
+                    // (INT8/INT4: 264 us against 267 without this, whose code costs more than it
+                    // spares)
+                    bool hidden = false, some = masked;
+                    if (WIN && KIND == 0 && masked) {
+                        const int k0 = j * kRows + c0, k1 = k0 + kPart - 1;
+                        hidden = k0 > pos_last ||
+                                 (p.window && k1 <= (int64_t)pos_first - p.window &&
+                                  k0 >= p.n_first);
+                        some = k1 > pos_first ||
+                               (p.window && k0 <= (int64_t)pos_last - p.window &&
+                                k1 >= p.n_first);
+                    }
+                    if (WIN && KIND == 0 && hidden) {
+                        uint32_t none[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            none[e] = 0;
+                        tmem_st32(tS + c0, none);
+                        tmem_st32(tS + c0 + kPart / 2, none);
+                    } else if constexpr (KIND != 0) {
                         quad_step<D, WIN>(
                             tS, tO, sk + c0, c0, valid - c0,
-                            (WIN ? masked : valid < kRows) || bad ? bad >> (c0 / kBlockTokens)
-                                                                  : -1,
+                            (WIN ? some : valid < kRows) || bad ? bad >> (c0 / kBlockTokens)
+                                                                : -1,
                             first, ms, ls,
                             [&]() {
                                 if (part == 1) {
@@ -1003,7 +995,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         tmem_landed<kPart>(s);
                         // scores in the log2 domain = s * mul
                         float mul = p.scale_log2;
-                        if (WIN && (masked || bad || mul < 0.f)) {
+                        if (WIN && (some || bad || mul <= 0.f)) {
                             uint32_t seen[2];
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
@@ -1013,10 +1005,15 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                 gone |= here & 2 ? 0xffff0000u : 0u;
                                 seen[w] = seen_keys(p, pos, j * kRows + c0 + 32 * w) & ~gone;
                             }
+                            if (mul <= 0.f) { // (the largest score is not the largest product)
+#pragma unroll
+                                for (int c = 0; c < kPart; ++c)
+                                    s[c] *= mul;
+                                mul = 1.f;
+                            }
 #pragma unroll
                             for (int c = 0; c < kPart; ++c)
-                                s[c] = (seen[c / 32] >> (c % 32)) & 1 ? s[c] * mul : -INFINITY;
-                            mul = 1.f;
+                                s[c] = (seen[c / 32] >> (c % 32)) & 1 ? s[c] : -INFINITY;
                         } else if (!WIN && (valid < kRows || bad || mul < 0.f)) {
                             const int here = valid - c0, bad_here = bad >> (c0 / kBlockTokens);
 #pragma unroll
@@ -1090,6 +1087,43 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     }
                     tmem_wait_st();
+                    if (L::kCheck && masked && part == 1) {
+                        // The rows of V that are not finite were zeroed in the tile (see there);
+                        // what this row sees of them joins its output at the end.
+                        const uint32_t fill = 2 * (n_tile + (uint32_t)(j - g.j0)) + 1;
+                        const volatile uint32_t *odd =
+                            reinterpret_cast<const uint32_t *>(smem + L::kOffOdd) + fill % SLOTS * 4;
+                        if (wait(kv_full + 8 * (fill % SLOTS), fill / SLOTS))
+    #pragma unroll 1
+                            for (int w = 0; w < kRows / 32; ++w) {
+                                uint32_t rows = odd[w];
+                                if (rows == 0)
+                                    continue;
+                                rows &= seen_keys(p, pos, j * kRows + 32 * w);
+    #pragma unroll 1
+                                for (; rows; rows &= rows - 1) {
+                                    const int key = j * kRows + 32 * w + __ffs(rows) - 1;
+                                    int blk = key / kBlockTokens;
+                                    blk += blk < g.span.kept ? 0 : g.span.skip;
+                                    const int64_t at =
+                                        (int64_t)__ldg(p.block_tables +
+                                                       (int64_t)walk.at.b * p.max_blocks + blk) *
+                                            p.n_kv + g.kvh;
+                                    const uint32_t *v = reinterpret_cast<const uint32_t *>(
+                                        static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                        (at * kBlockTokens + key % kBlockTokens) * D);
+                                    if (!poison)
+                                        for (int c = 0; c < D / 32; ++c)
+                                            poisons[c * kUnitRows] = 0;
+                                    poison = true;
+    #pragma unroll 1
+                                    for (int d = 0; d < D; ++d)
+                                        if ((v[d / 2] >> (d % 2 * 16) & 0x7f80u) == 0x7f80u)
+                                            poisons[d / 32 * kUnitRows] |= 1u << (d % 32);
+                                }
+                            }
+                        __syncwarp();
+                    }
                     tc_fence_before();
                     mbar_arrive(p_full + 16 * half + 8 * part);
                 }
@@ -1584,7 +1618,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         const uint32_t dst = ring + slot * TILE;
                         const uint8_t *raw = smem + L::kOffRaw + from * L::RAW;
                         const int mask = raw_mask[from];
-                        // rows of absent and bad blocks and behind the context are zero
+                        // rows of absent and bad blocks and behind the context have scales of zero
                         auto present = [&](int r) {
                             return r < valid && ((mask >> (r / kBlockTokens)) & 1);
                         };
@@ -1601,13 +1635,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         // Chunk t + i * CONV of the tile: its row moves by STEP, a multiple of the
                         // swizzle's eight, so the addresses move by constants.
                         uint32_t in = smem_u32(raw) + 16 * t, out = dst + t / CPR * 128;
+                        uint32_t next[4];
+                        lds128(in, next);
 #pragma unroll 1 // (unrolled, its instructions push the other warps' out of the cache)
                         for (int r = t / CPR; r < kRows; r += STEP) {
-                            uint32_t w[4];
-                            lds128(in, w);
-                            // rows that are not there are zero (INT4: 8 is code 0)
-                            if (!present(r))
-                                w[0] = w[1] = w[2] = w[3] = 0;
+                            // (rows that are not there have scales of zero, and any code is finite)
+                            const uint32_t w[4] = {next[0], next[1], next[2], next[3]};
+                            if (r + STEP < kRows)
+                                lds128(in + 16 * CONV, next);
                             if constexpr (KIND == 1) {
                                 // (a row's second 64 columns take its chunks in the other
                                 // order: a row's eight threads then write to different banks)
