@@ -720,6 +720,40 @@ __device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float 
         l[i] += sum[i].x + sum[i].y;
 }
 
+// WIN, bf16: notes in `poisons` the output columns that V rows which are not finite (bits of odd,
+// of the 128 keys from k0 on) spoil for a token at virtual position pos that sees them. Out of
+// line: it runs next to never, and inline it would stand in the softmax's loop.
+template <int D>
+__device__ __noinline__ bool note_odd(const CrossParams &p, const volatile uint32_t *odd,
+                                      uint32_t *poisons, bool poison, int pos, int k0, int b,
+                                      int kvh, int kept, int skip)
+{
+#pragma unroll 1
+    for (int w = 0; w < kRows / 32; ++w) {
+        uint32_t rows = odd[w] & seen_keys(p, pos, k0 + 32 * w);
+#pragma unroll 1
+        for (; rows; rows &= rows - 1) {
+            const int key = k0 + 32 * w + __ffs(rows) - 1;
+            int blk = key / kBlockTokens;
+            blk += blk < kept ? 0 : skip;
+            const int64_t at =
+                (int64_t)__ldg(p.block_tables + (int64_t)b * p.max_blocks + blk) * p.n_kv + kvh;
+            const uint32_t *v = reinterpret_cast<const uint32_t *>(
+                static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                (at * kBlockTokens + key % kBlockTokens) * D);
+            if (!poison)
+                for (int c = 0; c < D / 32; ++c)
+                    poisons[c * kUnitRows] = 0;
+            poison = true;
+#pragma unroll 1
+            for (int d = 0; d < D; ++d)
+                if ((v[d / 2] >> (d % 2 * 16) & 0x7f80u) == 0x7f80u)
+                    poisons[d / 32 * kUnitRows] |= 1u << (d % 32);
+        }
+    }
+    return poison;
+}
+
 template <int D, int KIND, bool WIN>
 __global__ void __launch_bounds__(Smem<D, KIND, WIN>::kThreads, 1)
 cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -914,10 +948,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // WIN: the virtual position of this thread's row (INT8/INT4: see quad_step)
             const int p0 = WIN ? g.p0() : 0;
             const int pos = p0 + ((two ? half * kRows + row : row) >> p.log2_g);
-            // ... and those of this warp's first and last row
-            const int warp_row = (two ? half * kRows : 0) + (row & ~31);
-            const int pos_first = p0 + (warp_row >> p.log2_g),
-                      pos_last = p0 + ((warp_row + 31) >> p.log2_g);
             bool poison = false; // this thread's row has seen a V entry that is not finite
             uint32_t *poisons = reinterpret_cast<uint32_t *>(smem + L::kOffPoison) + tid;
             uint32_t n_s = half ? n_b[1] : n_b[0];
@@ -952,31 +982,11 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 for (int part = 0; part < 2; ++part) {
                     const int c0 = part * kPart;
                     const bool first = part == 0 && j == j_first;
-                    // WIN: what this warp's rows see of the step: nothing, all, or some of it
-                    // (INT8/INT4: 264 us against 267 without this, whose code costs more than it
-                    // spares)
-                    bool hidden = false, some = masked;
-                    if (WIN && KIND == 0 && masked) {
-                        const int k0 = j * kRows + c0, k1 = k0 + kPart - 1;
-                        hidden = k0 > pos_last ||
-                                 (p.window && k1 <= (int64_t)pos_first - p.window &&
-                                  k0 >= p.n_first);
-                        some = k1 > pos_first ||
-                               (p.window && k0 <= (int64_t)pos_last - p.window &&
-                                k1 >= p.n_first);
-                    }
-                    if (WIN && KIND == 0 && hidden) {
-                        uint32_t none[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            none[e] = 0;
-                        tmem_st32(tS + c0, none);
-                        tmem_st32(tS + c0 + kPart / 2, none);
-                    } else if constexpr (KIND != 0) {
+                    if constexpr (KIND != 0) {
                         quad_step<D, WIN>(
                             tS, tO, sk + c0, c0, valid - c0,
-                            (WIN ? some : valid < kRows) || bad ? bad >> (c0 / kBlockTokens)
-                                                                : -1,
+                            (WIN ? masked : valid < kRows) || bad ? bad >> (c0 / kBlockTokens)
+                                                                  : -1,
                             first, ms, ls,
                             [&]() {
                                 if (part == 1) {
@@ -994,8 +1004,13 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         tmem_wait_ld();
                         tmem_landed<kPart>(s);
                         // scores in the log2 domain = s * mul
-                        float mul = p.scale_log2;
-                        if (WIN && (some || bad || mul <= 0.f)) {
+                        // (WIN: the products of a negative scale come negated; with none, masked
+                        // scores times 0 would not be numbers. A step of its own for those in
+                        // the softmax costs 160 us against 153 where most steps are masked.)
+                        float mul = !WIN                  ? p.scale_log2
+                                    : p.scale_log2 == 0.f ? 1.1754944e-38f
+                                                          : fabsf(p.scale_log2);
+                        if (WIN && (masked || bad)) {
                             uint32_t seen[2];
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
@@ -1004,12 +1019,6 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                 gone |= here & 1 ? 0x0000ffffu : 0u;
                                 gone |= here & 2 ? 0xffff0000u : 0u;
                                 seen[w] = seen_keys(p, pos, j * kRows + c0 + 32 * w) & ~gone;
-                            }
-                            if (mul <= 0.f) { // (the largest score is not the largest product)
-#pragma unroll
-                                for (int c = 0; c < kPart; ++c)
-                                    s[c] *= mul;
-                                mul = 1.f;
                             }
 #pragma unroll
                             for (int c = 0; c < kPart; ++c)
@@ -1092,37 +1101,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         // what this row sees of them joins its output at the end.
                         const uint32_t fill = 2 * (n_tile + (uint32_t)(j - g.j0)) + 1;
                         const volatile uint32_t *odd =
-                            reinterpret_cast<const uint32_t *>(smem + L::kOffOdd) + fill % SLOTS * 4;
-                        if (wait(kv_full + 8 * (fill % SLOTS), fill / SLOTS))
-    #pragma unroll 1
-                            for (int w = 0; w < kRows / 32; ++w) {
-                                uint32_t rows = odd[w];
-                                if (rows == 0)
-                                    continue;
-                                rows &= seen_keys(p, pos, j * kRows + 32 * w);
-    #pragma unroll 1
-                                for (; rows; rows &= rows - 1) {
-                                    const int key = j * kRows + 32 * w + __ffs(rows) - 1;
-                                    int blk = key / kBlockTokens;
-                                    blk += blk < g.span.kept ? 0 : g.span.skip;
-                                    const int64_t at =
-                                        (int64_t)__ldg(p.block_tables +
-                                                       (int64_t)walk.at.b * p.max_blocks + blk) *
-                                            p.n_kv + g.kvh;
-                                    const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                                        static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                                        (at * kBlockTokens + key % kBlockTokens) * D);
-                                    if (!poison)
-                                        for (int c = 0; c < D / 32; ++c)
-                                            poisons[c * kUnitRows] = 0;
-                                    poison = true;
-    #pragma unroll 1
-                                    for (int d = 0; d < D; ++d)
-                                        if ((v[d / 2] >> (d % 2 * 16) & 0x7f80u) == 0x7f80u)
-                                            poisons[d / 32 * kUnitRows] |= 1u << (d % 32);
-                                }
-                            }
-                        __syncwarp();
+                            reinterpret_cast<const uint32_t *>(smem + L::kOffOdd) +
+                            fill % SLOTS * 4;
+                        if (wait(kv_full + 8 * (fill % SLOTS), fill / SLOTS) &&
+                            (odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
+                            poison = note_odd<D>(p, odd, poisons, poison, pos, j * kRows,
+                                                 walk.at.b, g.kvh, g.span.kept, g.span.skip);
+                            __syncwarp();
+                        }
                     }
                     tc_fence_before();
                     mbar_arrive(p_full + 16 * half + 8 * part);
@@ -1151,7 +1137,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
             // 32 outputs from column c on, of a row whose weights sum to l
             auto emit = [&](int c, float (&o)[32], float inv) {
-                if (L::kCheck && poisoned) {
+                if (L::kCheck && __builtin_expect(poisoned, 0)) {
 #pragma unroll 1
                     for (int t = 0; t < 2; ++t) {
                         if (!((poisoned >> t) & 1))
@@ -1316,7 +1302,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // in its softmax while the other has the tensor cores; with a thread per buffer
             // they fall into step and both wait for both.
             if (elect_one()) {
-                constexpr uint32_t iS = tc_idesc_bf16(kRows, kRows, false);
+                const uint32_t iS =
+                    tc_idesc_bf16(kRows, kRows, false) |
+                    (WIN && KIND == 0 && p.scale_log2 < 0.f ? kNegateA : 0u);
                 constexpr uint32_t iO = tc_idesc_bf16(kRows, D, true);
                 constexpr uint64_t kHigh = tc_desc_high();
                 constexpr uint32_t kSlotDesc = TILE >> 4;

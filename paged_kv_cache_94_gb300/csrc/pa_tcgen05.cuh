@@ -117,6 +117,8 @@ constexpr uint32_t tc_idesc_bf16(int m, int n, bool b_mn)
            (uint32_t)(m >> 4) << 24;
 }
 
+constexpr uint32_t kNegateA = 1u << 13; // ... of -A
+
 // 32 columns of this warp's 32 lanes (a row per thread). The values may be used only
 // after tmem_wait_ld() and tmem_landed() on them.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v)
