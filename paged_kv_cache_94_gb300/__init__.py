@@ -539,15 +539,16 @@ _GEOMS: dict = {}
 
 def _pool(k_cache, v_cache, k_scale, v_scale, n_h, device):
     """Geometry of a pool and the pointers of its K, V and scales, checked."""
-    _need_cuda("k_cache", k_cache)
-    shape = k_cache.shape
-    key = (shape, k_cache.dtype, n_h)
+    if not isinstance(k_cache, torch.Tensor):
+        _need_cuda("k_cache", k_cache)
+    shape, dtype = k_cache.shape, k_cache.dtype
+    kp = _take("k_cache", k_cache, dtype, device)
+    key = (shape, dtype, n_h)
     g = _GEOMS.get(key)
     if g is None:
         g = geometry(k_cache, shape[1] if n_h is None and len(shape) == 4 else n_h)
         _GEOMS[key] = g
-    kp = _take("k_cache", k_cache, k_cache.dtype, device)
-    vp = _take("v_cache", v_cache, k_cache.dtype, device)
+    vp = _take("v_cache", v_cache, dtype, device)
     if v_cache.shape != shape:
         raise ValueError("v_cache must have the shape of k_cache")
     if g.kv_dtype == PA_KV_BF16:
@@ -775,7 +776,7 @@ def _ragged(what: str, q, cu_q, k_cache, v_cache, block_tables, context_lens, sc
     if d != g.d_h or context_lens.shape != (B,) or cu_q.shape != (B + 1,):
         raise ValueError("q, cu_q, block_tables, context_lens disagree on num_seqs or d_h")
     if out is not None:
-        _need_cuda("out", out, torch.bfloat16)
+        _take("out", out, torch.bfloat16, dev)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
     num_ctas = _int32("num_ctas", num_ctas)
@@ -789,6 +790,7 @@ def _ragged(what: str, q, cu_q, k_cache, v_cache, block_tables, context_lens, sc
         owned = _Owned(dev) if prepare else None
         if out is None:
             out = owned.empty(q.shape, q.dtype) if prepare else torch.empty_like(q)
+        args[at] = out.data_ptr()
         if workspace is None:
             key = ("cross", dev.index, d, num_ctas)
             nbytes = _WS_SIZES.get(key)
@@ -801,9 +803,10 @@ def _ragged(what: str, q, cu_q, k_cache, v_cache, block_tables, context_lens, sc
             counters = (nbytes // (512 * (d + 2) * 4) * 4 + 255) // 256 * 256
             workspace = (owned.workspace(nbytes, counters) if prepare else
                          _stream_workspace("cross", nbytes, counters, dev, handle))
-        args[at] = _take("out", out, torch.bfloat16, dev)
-        args[at + 1] = _take("workspace", workspace, workspace.dtype, dev)
-        args[at + 2] = workspace.numel() * workspace.element_size()
+            args[at + 1], args[at + 2] = workspace.data_ptr(), nbytes
+        else:
+            args[at + 1] = _take("workspace", workspace, workspace.dtype, dev)
+            args[at + 2] = workspace.numel() * workspace.element_size()
         return _issue(getattr(_lib(), what), args, at + 5, what, out, handle, stream, dev, owned)
 
 
@@ -872,7 +875,9 @@ def pa_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
         if out is None:
             out = (owned.empty((T, n_h, d), q.dtype) if prepare else
                    torch.empty((T, n_h, d), dtype=q.dtype, device=dev))
-        args[15] = _take("out", out, torch.bfloat16, dev)
+            args[15] = out.data_ptr()
+        else:
+            args[15] = _take("out", out, torch.bfloat16, dev)
         return _issue(_lib().pa_rope_write, args, 22, "pa_rope_write", out, _stream_handle(dev),
                       stream, dev, owned)
 
@@ -922,7 +927,7 @@ def pa_window_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if d != g.d_h or tables != B or context_lens.shape != (B,):
         raise ValueError("q, block_tables, context_lens disagree on num_seqs or d_h")
     if out is not None:
-        _need_cuda("out", out, torch.bfloat16)
+        _take("out", out, torch.bfloat16, dev)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
     num_ctas = _int32("num_ctas", num_ctas)
@@ -936,6 +941,7 @@ def pa_window_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         owned = _Owned(dev) if prepare else None
         if out is None:
             out = owned.empty(q.shape, q.dtype) if prepare else torch.empty_like(q)
+        args[12] = out.data_ptr()
         if workspace is None:
             key = ("window", dev.index, g.num_blocks, n_h, g.n_kv, d, g.kv_dtype, B, num_ctas)
             nbytes = _WS_SIZES.get(key)
@@ -947,9 +953,10 @@ def pa_window_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
             counters = _counter_bytes(g, B)
             workspace = (owned.workspace(nbytes, counters) if prepare else
                          _stream_workspace("window", nbytes, counters, dev, handle))
-        args[12] = _take("out", out, torch.bfloat16, dev)
-        args[13] = _take("workspace", workspace, workspace.dtype, dev)
-        args[14] = workspace.numel() * workspace.element_size()
+            args[13], args[14] = workspace.data_ptr(), nbytes
+        else:
+            args[13] = _take("workspace", workspace, workspace.dtype, dev)
+            args[14] = workspace.numel() * workspace.element_size()
         return _issue(_lib().pa_window_decode, args, 17, "pa_window_decode", out, handle, stream,
                       dev, owned)
 
