@@ -1,5 +1,6 @@
 // Cross attention: any number of query tokens per sequence over a paged K/V cache
-// of another length (an encoder's states, or rows an eviction kept).
+// of another length (an encoder's states, or rows an eviction kept). With WIN the same kernel
+// attends causally within a window and to a sequence's first tokens (pa_window.cu says how).
 //
 //     s_j = scale <q[t][h], K_b[j][h / g]>,  j < ctx_b (no mask)
 //     out[t][h] = sum_j softmax(s)_j V_b[j][h / g],  cu_q[b] <= t < cu_q[b + 1]

@@ -7,19 +7,19 @@
 //
 // Angles. In 32 bits position * inv_freq of a far position has lost the angle (2^20 rad: steps
 // of 1/16). Here a frequency is a 64-bit fraction of a turn, and its product with the position
-// modulo 2^64 drops whole turns exactly. What is left, less whole quarters, is rounded once to
-// fp32 (an angle below pi / 4, 2^-24 relative).
+// modulo 2^64 drops whole turns exactly. What is left, less whole quarters, is an angle of up to
+// pi / 4 in fp32, whose sine and cosine need a few products.
 //
 // What bounds it: memory for prompts (each row read once and written once), latency for a
 // decode step. A thread takes 16 values of a row, both halves of its eight pairs, as two
 // 16-byte loads, the same ones of every row that it comes to; a CTA some tokens, whose sines
 // and cosines it works out once for all heads while the first rows are on their way.
 //
-// Measured on a GB300: 8192 tokens of 32 + 8 heads of 128 into a bf16 pool 39 us, 5170 GB/s,
-// 0.76 of the measured copy rate (56 with rows found by division and 98 registers, two CTAs
-// per SM); into an INT8 pool 43. 4111 tokens of 16 + 16 heads of 64 into an INT8 pool 13.5 us
-// (21.5 where one near half had all eight values divided, 18.7 with a division each). A step
-// of 64 tokens 2.9 us.
+// Measured on a GB300, launches back to back: 8192 tokens of 32 + 8 heads of 128 into a bf16
+// pool 37.7 us, 5340 GB/s, 0.79 of the measured copy rate (56 with rows found by division and
+// 98 registers, two CTAs per SM; 39 with angles in double precision); into an INT8 pool 42.
+// 4111 tokens of 16 + 16 heads of 64 into an INT8 pool 13.1 us (21.5 where one near half had
+// all eight values divided, 18.7 with a division each). A step of 64 tokens 2.8 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -51,19 +51,43 @@ struct RopeParams {
     int32_t round_rows, round_tokens; // how far a thread's row moves from round to round
 };
 
-// cos and sin of position * freq, freq in radians per position.
+// freq (radians per position) in turns, times 2^64 and modulo 2^64. In integers: a CTA's few
+// multiplications in double precision would keep that unit, a 64th as fast, busy for 800 cycles.
+// freq = m 2^(e - 52), 1 / (2 pi) = c 2^-64 within 2^-62 of itself: m c 2^(e - 52).
+__device__ __forceinline__ uint64_t turn_step(double freq)
+{
+    const uint64_t bits = (uint64_t)__double_as_longlong(freq);
+    const int e = (int)(bits >> 52 & 0x7ff) - 1023;
+    const uint64_t m = (bits & 0xfffffffffffffull) | 1ull << 52, c = 0x28be60db9391054aull;
+    const uint64_t lo = m * c, hi = __umul64hi(m, c);
+    const int right = 52 - e; // how far the product moves
+    uint64_t x;
+    if (right >= 128 || right <= -64)
+        x = 0;
+    else if (right >= 64)
+        x = hi >> (right - 64);
+    else if (right > 0)
+        x = lo >> right | hi << (64 - right);
+    else
+        x = lo << -right;
+    return (bits >> 63) ? 0 - x : x;
+}
+
+// cos and sin of position * freq.
 __device__ __forceinline__ float2 turn_of(int32_t position, double freq, float amplitude)
 {
-    const double turns = freq * 0.15915494309189533577; // 1 / (2 pi)
-    if (!(fabs(turns) < 4.5e15)) // no fraction left, or not a number
+    if ((__double2hiint(freq) & 0x7ff00000) == 0x7ff00000) // not finite
         return make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
-    const int64_t step = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-    const uint64_t at = (uint64_t)(int64_t)position * (uint64_t)step;
+    const uint64_t at = (uint64_t)(int64_t)position * turn_step(freq);
     const uint64_t quarter = (at + (1ull << 61)) >> 62; // nearest
-    // half turns, -1/4 .. 1/4
-    const float x = (float)(int64_t)(at - (quarter << 62)) * 1.0842021724855044e-19f; // 2^-63
-    float s, c;
-    sincospif(x, &s, &c);
+    // The rest, up to pi / 4 either way, and the Taylor series of its sine up to x^9 and of its
+    // cosine up to x^10: what is left out is below 2^-28.
+    const float x = (float)(int64_t)(at - (quarter << 62)) * 3.4061215800304075e-19f; // 2 pi 2^-64
+    const float z = x * x;
+    float s = fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -1.6666667e-1f);
+    s = fmaf(x * z, s, x);
+    float c = fmaf(z, fmaf(z, fmaf(z, -2.7557319e-7f, 2.4801587e-5f), -1.3888889e-3f), 4.1666667e-2f);
+    c = fmaf(z, fmaf(z, c, -0.5f), 1.f);
     if (quarter & 1) {
         const float t = c;
         c = -s;
@@ -303,12 +327,14 @@ cudaError_t launch_of(const RopeParams &p, int sms, cudaStream_t stream)
             <<<dim3((unsigned)p.num_tokens, (unsigned)rounds), kThreads,
                p.pairs * sizeof(float2), stream>>>(r);
     } else {
-        // Tokens of a CTA, up to a sine and cosine to a thread: the fewest rounds, and one for
-        // the CTA's start, over all waves of four CTAs to an SM.
+        // Tokens of a CTA, up to four sines and cosines to a thread: the fewest rounds, those of
+        // the sines included, over all waves of four CTAs to an SM (4 + 1 heads of 128, 30000
+        // tokens: 25 us against 34 with four tokens).
         int64_t best = INT64_MAX;
-        for (int t = 1; t <= kThreads / p.pairs; ++t) {
+        for (int t = 1; t <= 4 * kThreads / p.pairs; ++t) {
             const int64_t waves = (p.num_tokens + (int64_t)t * 4 * sms - 1) / ((int64_t)t * 4 * sms);
-            const int64_t cost = waves * (((int64_t)t * p.rows + 2 * STEP - 1) / (2 * STEP) + 1);
+            const int64_t cost = waves * (((int64_t)t * p.rows + 2 * STEP - 1) / (2 * STEP) +
+                                          (t * p.pairs + kThreads - 1) / kThreads);
             if (cost < best) {
                 best = cost;
                 r.tokens = t;
