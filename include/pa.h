@@ -539,10 +539,12 @@ pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t 
  *   window, n_first  >= 0 (PA_ERR_SHAPE)
  * Block-table entries of blocks that no new token of the sequence sees are not read: those
  * between the block of position n_first - 1 and the first one of the first new token's
- * window may have been given back. K and V that a token does not see do not reach its row,
+ * window may have been given back (pa_allocator_free on them, and the sequence goes on
+ * appending). K and V that a token does not see do not reach its row,
  * whatever they hold; entries that are not finite make infinity or NaN of what sees them.
  * Every other argument is pa_cross_attention's, the workspace's size
- * pa_window_attention_workspace_size(geom, num_ctas). Accumulation and the weights'
+ * pa_window_attention_workspace_size(geom, num_ctas); out meets no memory of q
+ * (PA_ERR_SHAPE). Accumulation and the weights'
  * precision are pa_cross_attention's too; results do not depend on how the work was split
  * beyond fp32 rounding, and are the same from call to call.
  */
@@ -568,9 +570,9 @@ size_t pa_window_attention_workspace_size(pa_geom geom, int32_t num_ctas);
  *
  *   window, n_first  >= 0 (PA_ERR_SHAPE)
  *   num_ctas         0: one wave of resident CTAs; > 0: that many
- * Every other argument and error is pa_decode's; the workspace is
- * pa_window_decode_workspace_size(geom, num_seqs, num_ctas) bytes, zeroed as
- * pa_decode_workspace_init says.
+ * Every other argument and error is pa_decode's, and out meets no memory of q
+ * (PA_ERR_SHAPE); the workspace is pa_window_decode_workspace_size(geom, num_seqs, num_ctas)
+ * bytes, zeroed as pa_decode_workspace_init says.
  */
 pa_status pa_window_decode(const void *q, const void *k_cache, const void *v_cache,
                            const float *k_scale, const float *v_scale,

@@ -30,6 +30,13 @@ using pa::DecodeParams;
 constexpr int kMaxSeqs = 8192;
 constexpr int kMaxCrossCtas = 8192;
 
+// Whether two runs of bytes meet.
+bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int group_of(const pa_geom &g) { return g.n_h / g.n_kv; }
@@ -383,6 +390,10 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
         !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
         return PA_ERR_ALIGNMENT;
 
+    const int64_t rows = (int64_t)num_seqs * g.n_h * g.d_h * 2;
+    if (wa && meet(out, rows, q, rows)) // (a split sequence's queries are read at several times)
+        return PA_ERR_SHAPE;
+
     if (ma && (!ma->mass || !ma->mass_out))
         return PA_ERR_NULL;
     if (ma && (!aligned(ma->mass, 16) || !aligned(ma->mass_out, 16)))
@@ -530,6 +541,9 @@ pa_status cross_impl(const void *q, int64_t num_q, const int32_t *cu_q, const vo
         !aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
         !aligned(workspace, 256) || (i8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
         return PA_ERR_ALIGNMENT;
+    const int64_t rows = num_q * geom.n_h * geom.d_h * 2;
+    if (wa && meet(out, rows, q, rows)) // (a split unit's queries are read at several times)
+        return PA_ERR_SHAPE;
     int dev, sms;
     if ((st = current_device(dev, sms)) != PA_OK)
         return st;
@@ -926,11 +940,9 @@ pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t 
         !aligned(slot_mapping, 8) || (i8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
         return PA_ERR_ALIGNMENT;
     // out is q itself, or apart from all that is read
-    const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), row = (uintptr_t)geom.d_h * 2;
-    const uintptr_t o1 = o0 + (uintptr_t)num_tokens * geom.n_h * row;
-    auto meets = [&](const void *x, int64_t stride, int heads) {
-        const uintptr_t x0 = reinterpret_cast<uintptr_t>(x);
-        return x0 < o1 && o0 < x0 + (uintptr_t)(num_tokens - 1) * stride * 2 + heads * row;
+    auto meets = [&](const void *x, int64_t stride, int64_t heads) {
+        return meet(out, num_tokens * geom.n_h * geom.d_h * 2, x,
+                    (num_tokens - 1) * stride * 2 + heads * geom.d_h * 2);
     };
     const bool in_place = out == q && (q_stride == (int64_t)geom.n_h * geom.d_h || num_tokens == 1);
     if ((!in_place && meets(q, q_stride, geom.n_h)) || meets(k, k_stride, geom.n_kv) ||

@@ -85,12 +85,16 @@ def turned(x, positions, inv_freq, axis, adjacent, amplitude):
     x = x.clone()
     tol = torch.zeros_like(x)
     pairs = len(inv_freq)
-    for i in range(pairs):
-        a, b = (2 * i, 2 * i + 1) if adjacent else (i, i + pairs)
-        angle = positions[int(axis[i])].numpy().astype(np.longdouble) * np.longdouble(float(inv_freq[i]))
-        cos = torch.from_numpy(np.cos(angle).astype(np.float64))[:, None] * amplitude
-        sin = torch.from_numpy(np.sin(angle).astype(np.float64))[:, None] * amplitude
-        u, w = x[:, :, a].clone(), x[:, :, b].clone()
-        x[:, :, a], x[:, :, b] = u * cos - w * sin, w * cos + u * sin
-        tol[:, :, a] = tol[:, :, b] = 2.0 ** -21 * (u.abs() + w.abs()) * abs(amplitude)
+    # (an angle in 64 bits is off by 2^-53 of itself: too much for positions far out only)
+    wide = np.longdouble if int(positions.abs().max() if positions.numel() else 0) > 1 << 21 or \
+        int(positions.min() if positions.numel() else 0) < -(1 << 21) else np.float64
+    at = positions.numpy().astype(wide)[np.asarray([int(a) for a in axis])]
+    angle = (at * np.asarray([float(f) for f in inv_freq], dtype=wide)[:, None]).T  # [T, pairs]
+    cos = torch.from_numpy(np.cos(angle).astype(np.float64))[:, None] * amplitude
+    sin = torch.from_numpy(np.sin(angle).astype(np.float64))[:, None] * amplitude
+    a, b = (slice(0, 2 * pairs, 2), slice(1, 2 * pairs, 2)) if adjacent else \
+        (slice(0, pairs), slice(pairs, 2 * pairs))
+    u, w = x[..., a].clone(), x[..., b].clone()
+    x[..., a], x[..., b] = u * cos - w * sin, w * cos + u * sin
+    tol[..., a] = tol[..., b] = 2.0 ** -21 * (u.abs() + w.abs()) * abs(amplitude)
     return x, tol
