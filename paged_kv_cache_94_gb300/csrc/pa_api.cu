@@ -456,8 +456,7 @@ pa_status decode_impl(const void *q, const void *k_cache, const void *v_cache, c
     p.num_ctas = grid;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.window = wa ? wa->window : o.window;
-    p.n_first = wa ? wa->n_first : 0;
-    p.n_sink = o.n_sink;
+    p.n_sink = wa ? wa->n_first : o.n_sink;
     p.sink_k = static_cast<const __nv_bfloat16 *>(o.n_sink > 0 ? o.sink_k : nullptr);
     p.sink_v = static_cast<const __nv_bfloat16 *>(o.n_sink > 0 ? o.sink_v : nullptr);
     p.g = group_of(g);

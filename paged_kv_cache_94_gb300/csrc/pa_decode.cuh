@@ -68,7 +68,8 @@ struct DecodeParams {
     int32_t num_ctas;
     float scale_log2;            // softmax scale * log2(e)
     int32_t window;              // > 0: attend the last `window` tokens only
-    int32_t n_sink;              // INT8: positions < n_sink read the bf16 sink rows
+    int32_t n_sink;              // INT8: positions < n_sink read the bf16 sink rows; pass 1:
+                                 // positions < n_sink are attended besides the window
     const __nv_bfloat16 *sink_k; // [B][n_kv][n_sink][D]
     const __nv_bfloat16 *sink_v;
     int32_t g;                   // query heads per kv head
@@ -93,8 +94,6 @@ struct DecodeParams {
     // row's softmax base and 1 / sum to ml[b][head].
     float *scores;
     float2 *ml;
-    // A window with first tokens (PASS 1): besides the window, positions < n_first are attended.
-    int32_t n_first;
 };
 
 // Pass 0: decode of each sequence; pass 1: the same over a window and the
@@ -136,11 +135,11 @@ __device__ __forceinline__ int32_t seq_first_block(const DecodeParams &p, int32_
 // Pass 1 reads a sequence as if its blocks between those of its first tokens and
 // its window's were not there: virtual block i is block i up to the former and
 // block i + skipped_blocks() behind them. What a token does not see is then one
-// hole, [n_first, the window's start), of at most 30 virtual positions: the rest of
+// hole, [n_sink, the window's start), of at most 30 virtual positions: the rest of
 // the last block of first tokens and the front of the window's first block.
 __device__ __forceinline__ int32_t kept_blocks(const DecodeParams &p)
 {
-    return p.n_first / kBlockTokens + (p.n_first % kBlockTokens ? 1 : 0);
+    return p.n_sink / kBlockTokens + (p.n_sink % kBlockTokens ? 1 : 0);
 }
 
 __device__ __forceinline__ int32_t skipped_blocks(const DecodeParams &p, int32_t ctx)

@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
             const int32_t gone = skipped_blocks(p, ctx_next) * kBlockTokens;
             ctx = ctx_next - gone;
             ws = window_start(p, ctx_next) - gone;
-            pool_from = min(p.n_first, ws);
+            pool_from = min(p.n_sink, ws);
             fb = 0;
         } else {
             ctx = ctx_next;
