@@ -11,7 +11,7 @@ size_t cross_workspace_bytes(int d_h, int num_ctas)
 cudaError_t launch_cross(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                          const CrossArgs &a, cudaStream_t stream)
 {
-    return launch_any<false>(tq, tk, tv, a, stream);
+    return launch_any<0>(tq, tk, tv, a, stream);
 }
 
 } // namespace pa

@@ -1,6 +1,7 @@
 // Cross attention: any number of query tokens per sequence over a paged K/V cache
 // of another length (an encoder's states, or rows an eviction kept). With WIN the same kernel
-// attends causally within a window and to a sequence's first tokens (pa_window.cu says how).
+// attends causally within a window and to a sequence's first tokens (pa_window.cu says how);
+// with WIN = 2 it does so for few tokens a sequence (see launch_any).
 //
 //     s_j = scale <q[t][h], K_b[j][h / g]>,  j < ctx_b (no mask)
 //     out[t][h] = sum_j softmax(s)_j V_b[j][h / g],  cu_q[b] <= t < cu_q[b + 1]
@@ -185,7 +186,7 @@ __device__ __forceinline__ int64_t line_before(const CrossParams &p, const Seq &
 }
 
 // Positions of one kv head.
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ int64_t head_length(const CrossParams &p, const Seq &s)
 {
     if constexpr (!WIN) {
@@ -199,7 +200,7 @@ __device__ __forceinline__ int64_t head_length(const CrossParams &p, const Seq &
     }
 }
 
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ int64_t seq_length(const CrossParams &p, const Seq &s)
 {
     if constexpr (!WIN)
@@ -209,7 +210,7 @@ __device__ __forceinline__ int64_t seq_length(const CrossParams &p, const Seq &s
 }
 
 // Sequence b's sizes; bad ones (reported where `report`) count as nothing.
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ Seq load_seq(const CrossParams &p, int b, bool report)
 {
     Seq s;
@@ -267,7 +268,7 @@ struct Start {
 };
 
 // The segments of the items at positions [start, hi) of the line, one after another.
-template <bool WIN>
+template <int WIN>
 struct Walk {
     const CrossParams &p;
     int64_t hi;
@@ -382,7 +383,7 @@ __device__ __forceinline__ int64_t line_ctas(const CrossParams &p, int64_t total
     return total == 0 ? 0 : max((int64_t)1, plan_ctas(p.num_ctas, total / kWeight2));
 }
 
-template <int D, int KIND, bool WIN>
+template <int D, int KIND, int WIN>
 struct Smem {
     static constexpr int TILE = kRows * D * 2; // one Q half, K tile or V tile in bf16
     static constexpr int kThreads = KIND ? (kCopyWarp + 1 + kConvWarps) * 32 : 384;
@@ -583,7 +584,7 @@ __device__ __forceinline__ uint32_t seen_keys(const CrossParams &q, int p, int k
 //   wait_o  O is complete
 // WIN: bad alone says whether keys are masked. The thread's first row is row `row` of the unit,
 // whose first token has virtual position p0; the step's first key is k0.
-template <int D, bool WIN, class WaitO>
+template <int D, int WIN, class WaitO>
 __device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float *sk, int c0,
                                           int here, int bad, bool first, float (&m)[4],
                                           float (&l)[4], WaitO wait_o, const CrossParams &p,
@@ -755,7 +756,7 @@ __device__ __noinline__ bool note_odd(const CrossParams &p, const volatile uint3
     return poison;
 }
 
-template <int D, int KIND, bool WIN>
+template <int D, int KIND, int WIN>
 __global__ void __launch_bounds__(Smem<D, KIND, WIN>::kThreads, 1)
 cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const CrossParams p)
@@ -949,12 +950,20 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // WIN: the virtual position of this thread's row (INT8/INT4: see quad_step)
             const int p0 = WIN ? g.p0() : 0;
             const int pos = p0 + ((two ? half * kRows + row : row) >> p.log2_g);
+            // WIN = 2: a warp whose rows are all behind the unit's last one. Whatever its scores hold
+            // as weights stays in its own rows.
+            const bool idle = (two ? half * kRows : 0) + (row & ~31) >= g.rows;
             bool poison = false; // this thread's row has seen a V entry that is not finite
             uint32_t *poisons = reinterpret_cast<uint32_t *>(smem + L::kOffPoison) + tid;
             uint32_t n_s = half ? n_b[1] : n_b[0];
             for (int j = j_first; j < g.j1; j += step, ++n_s) {
                 if (!wait(s_full + 8 * half, n_s))
                     break;
+                if (WIN == 2 && idle) { // nothing to form
+                    mbar_arrive(p_full + 16 * half);
+                    mbar_arrive(p_full + 16 * half + 8);
+                    continue;
+                }
                 tc_fence_after();
                 const int bad = half_mask[half];
                 const int valid = min(ctx - j * kRows, kRows);
@@ -1425,11 +1434,18 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     WIN ? g.span.blocks
                         : (int)(((int64_t)walk.s.ctx + kBlockTokens - 1) / kBlockTokens);
                 const int32_t *table = p.block_tables + (int64_t)walk.at.b * p.max_blocks;
-                for (int j = g.j0; j < g.j1; ++j) {
-                    // lanes 0-7 (and their copies): the tile's eight blocks
+                // lanes 0-7 (and their copies): the eight blocks of tile j
+                auto entry = [&](int j) {
                     const int blk = j * kTileBlocks + (lane & 7);
                     const int gap = WIN && blk >= g.span.kept ? g.span.skip : 0;
-                    const int32_t phys = blk < nblk ? __ldg(table + blk + gap) : -1;
+                    return blk < nblk ? __ldg(table + blk + gap) : -1;
+                };
+                int32_t next = WIN == 2 ? entry(g.j0) : 0; // loaded a tile ahead
+                for (int j = g.j0; j < g.j1; ++j) {
+                    const int blk = j * kTileBlocks + (lane & 7);
+                    const int32_t phys = WIN == 2 ? next : entry(j);
+                    if (WIN == 2 && j + 1 < g.j1)
+                        next = entry(j + 1);
                     const bool ok = phys >= 0 && phys < p.num_blocks;
                     const uint32_t bad =
                         __ballot_sync(0xffffffffu, blk < nblk && !ok) & 0xffu;
@@ -1670,7 +1686,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         tmem_dealloc(tmem, 512);
 }
 
-template <int D, int KIND, bool WIN>
+template <int D, int KIND, int WIN>
 cudaError_t launch_of(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                       const CrossParams &p, cudaStream_t stream)
 {
@@ -1689,7 +1705,7 @@ cudaError_t launch_of(const CUtensorMap &tq, const CUtensorMap &tk, const CUtens
 
 size_t counter_bytes(int num_ctas) { return ((size_t)num_ctas * 4 + 255) / 256 * 256; }
 
-template <bool WIN>
+template <int WIN>
 cudaError_t launch_any(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                        const CrossArgs &a, cudaStream_t stream)
 {
@@ -1717,6 +1733,13 @@ cudaError_t launch_any(const CUtensorMap &tq, const CUtensorMap &tk, const CUten
     p.window = a.window;
     p.n_first = a.n_first;
     const int kind = a.kind;
+    // Few tokens: on average no more than a half's rows to a (sequence, kv head). Their warps
+    // without rows then do nothing and the block table is read a tile ahead: 48 drafts of 1..8
+    // tokens 119 us against 127, prompts of a long sequence 2090 against 2050.
+    if constexpr (WIN == 1)
+        if (kind == 0 && a.num_q * a.g <= (int64_t)a.num_seqs * kRows)
+            return a.d_h == 128 ? launch_of<128, 0, 2>(tq, tk, tv, p, stream)
+                                : launch_of<64, 0, 2>(tq, tk, tv, p, stream);
     if (a.d_h == 128)
         return kind == 0   ? launch_of<128, 0, WIN>(tq, tk, tv, p, stream)
                : kind == 1 ? launch_of<128, 1, WIN>(tq, tk, tv, p, stream)

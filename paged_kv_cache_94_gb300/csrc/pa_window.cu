@@ -22,8 +22,8 @@
 // Measured on a GB300 (g = 4, d_h 128, bf16 unless said): one prompt of 16384 tokens 2050 us,
 // 1070 TFLOP/s with each product counted once: with those for both parts of the weights 1610,
 // 0.95 of what the power cap sustains (1698). Eight chunks of 512..2048 tokens over 2048..8192
-// with a window of 4096: 647..665 us, 980 TFLOP/s. 48 drafts of 1..8 tokens over 200..8192: 127
-// us, 4870 GB/s, 0.72 of the measured copy rate. 24 prompts of 33..1999 tokens, 16 heads of 64, g
+// with a window of 4096: 647..665 us, 980 TFLOP/s. 48 drafts of 1..8 tokens over 200..8192: 119
+// us, 5210 GB/s, 0.77 of the measured copy rate. 24 prompts of 33..1999 tokens, 16 heads of 64, g
 // = 1, a window of 333: 147..155 us, where nearly every tile is masked and a unit has five.
 // INT8, 16..256 tokens over 512..8192, g = 1, a window of 2000: 259 us, bound by the instruction
 // cache: weights and codes in fp16, a quarter fewer instructions but two loops more, took 279.
@@ -34,7 +34,7 @@ namespace pa {
 cudaError_t launch_window(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CrossArgs &a, cudaStream_t stream)
 {
-    return launch_any<true>(tq, tk, tv, a, stream);
+    return launch_any<1>(tq, tk, tv, a, stream);
 }
 
 } // namespace pa
