@@ -48,6 +48,7 @@
 // loads, unit ends and merges.
 #pragma once
 
+#include "pa_check.h"
 #include "pa_decode.cuh"
 #include "pa_launch.h"
 #include "pa_tcgen05.cuh"
@@ -1541,20 +1542,20 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // ============================================= V rows that are not finite
             // A weight of 0 times infinity or NaN is NaN: in tiles with keys that some row
             // does not see, such entries would reach rows that they must not. The two warps
-            // take turns at those tiles: they zero the entries and note their rows, and the
-            // softmax puts NaN into the outputs of the rows that do see them.
-            uint32_t n_tile = 0, phases = 0, turn = 0;
+            // share those tiles: they zero the entries and note their rows, and the softmax puts
+            // NaN into the outputs of the rows that do see them. A slot's tiles all go to one
+            // warp, which waits for no other: see pa_check.h.
+            static_assert(SLOTS % 4 == 0, "a slot's tiles go to one warp");
+            const uint32_t mine = warp - kCopyWarp - 1;
+            uint32_t n_tile = 0, phases = 0;
             while (walk.next(g) && !dead) {
                 for (int j = g.j0; j < g.j1 && !dead; ++j, ++n_tile) {
-                    if (!g.masked(p, j))
+                    if (check_warp(n_tile) != mine || !g.masked(p, j))
                         continue;
-                    const uint32_t slot = (2 * n_tile + 1) % SLOTS;
-                    // (each of them waits for every one, so that a phase is never two ahead)
+                    const uint32_t slot = check_slot(n_tile, SLOTS);
                     if (!wait(landed + 8 * slot, phases >> slot))
                         break;
                     phases ^= 1u << slot;
-                    if ((turn++ & 1) != (uint32_t)(warp - kCopyWarp - 1))
-                        continue;
                     const uint32_t tile = ring + slot * TILE;
                     uint32_t sum[2] = {0, 0};
 #pragma unroll 4
