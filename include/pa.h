@@ -567,6 +567,10 @@ size_t pa_window_attention_workspace_size(pa_geom geom, int32_t num_ctas);
  * (pa_decode_opt's window has no first tokens: its n_sink are bf16 rows of positions inside
  * the window.) Block-table entries of blocks wholly between the two are not read: a
  * windowed cache may have given them back.
+ * Over INT8 and INT4 pools a weight times its V scale enters the products as one fp16 value
+ * (2^-11 relative, or 2^-25 of the largest scale's), in two parts (2^-21) with 32 tokens of
+ * which a value may pass 8 in magnitude: results stay within 1e-2 (1 + |ref|) where V rows of
+ * many magnitudes cancel. pa_decode has one part, whatever the values.
  *
  *   window, n_first  >= 0 (PA_ERR_SHAPE)
  *   num_ctas         0: one wave of resident CTAs; > 0: that many

@@ -29,7 +29,9 @@
 // max|Q'| < 2^15: the bf16 -> fp16 conversion is then exact for every
 // normal value. W = p * v_scale[tok] / s_base, where s_base is a running
 // V-scale base that only moves (rescaling O) when a block's largest V scale
-// exceeds it 64-fold, so W <= 2^8 * 2^6 stays far below fp16's maximum.
+// exceeds it 64-fold, so W <= 2^8 * 2^6 stays far below fp16's maximum. W is one
+// fp16 value, off by up to 2^-11 of itself; over a window and first tokens (HOLE)
+// its remainder is a second one where values are large (kWideValue).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -175,6 +177,12 @@ struct QuantMmaPolicy {
     static constexpr int QBYTES = 0;
     static constexpr uint32_t TX = STAGE + EXTRA;
     static constexpr float kScaleRatio = 64.f;     // V-scale base moves beyond this
+    // Weights in two fp16 parts (HOLE). One part is off by 2^-11 of itself, an output by up to
+    // 2^-11 of the weighted mean of |v|: for values up to kWideValue 0.004, well inside 1e-2 (1 +
+    // |out|); for V rows over six decades that cancel to a small output it is not. Where no item
+    // is wide the test costs 0..1 us of 90, where all are a quarter more time (89 -> 110 us).
+    static constexpr float kWideValue = 8.f;
+    static constexpr float kTopCode = BITS == 8 ? 128.f : 8.f;
     using Layout = SmemLayout<D, GQ, NW, S, STAGE, EXTRA, QBYTES>;
 
     struct State {
@@ -565,6 +573,10 @@ struct QuantMmaPolicy {
         }
         // W^T as B fragments (tokens x heads): transpose of the score layout.
         uint32_t pb0[BPI][NT], pb1[BPI][NT];
+        uint32_t pl0[HOLE ? BPI : 1][HOLE ? NT : 1], pl1[HOLE ? BPI : 1][HOLE ? NT : 1];
+        // HOLE: an item with values that may pass kWideValue takes its weights in two parts, the
+        // second one first.
+        const bool wide = HOLE && __any_sync(0xffffffffu, svm * kTopCode > kWideValue);
 #pragma unroll
         for (int j = 0; j < BPI; ++j) {
             const float r_lo = sv_lo[j] * st.sinv, r_hi = sv_hi[j] * st.sinv;
@@ -574,10 +586,33 @@ struct QuantMmaPolicy {
                 const uint32_t w1 = pack_f16x2(pr[j][nt][2] * r_hi, pr[j][nt][3] * r_hi);
                 pb0[j][nt] = movmatrix_trans(w0);
                 pb1[j][nt] = movmatrix_trans(w1);
+                if constexpr (HOLE) {
+                    if (wide) {
+                        float h[4];
+                        h2_to_f2(w0, h[0], h[1]);
+                        h2_to_f2(w1, h[2], h[3]);
+                        pl0[j][nt] = movmatrix_trans(pack_f16x2(fmaf(pr[j][nt][0], r_lo, -h[0]),
+                                                                fmaf(pr[j][nt][1], r_lo, -h[1])));
+                        pl1[j][nt] = movmatrix_trans(pack_f16x2(fmaf(pr[j][nt][2], r_hi, -h[2]),
+                                                                fmaf(pr[j][nt][3], r_hi, -h[3])));
+                    }
+                }
             }
         }
+        if constexpr (HOLE) {
+            if (wide)
+                weigh(st, kt, pl0, pl1);
+        }
+        weigh(st, kt, pb0, pb1);
+    }
 
-        // ---- O^T += Vcode^T . W^T, one k-step per block. Thread rows
+    // O^T += Vcode^T . W^T over one item.
+    __device__ static void weigh(State &st, uint32_t kt, const uint32_t (&pb0)[BPI][NT],
+                                 const uint32_t (&pb1)[BPI][NT])
+    {
+        const int lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
+
+        // One k-step per block. Thread rows
         // (tokens) 2t, 2t+1, 2t+8, 2t+9 of the block; its d values are
         // CW*gid + 2*mt + r for row tile mt, r = 0 (A rows gid) or 1 (A rows
         // gid+8): CW contiguous codes of each token row.

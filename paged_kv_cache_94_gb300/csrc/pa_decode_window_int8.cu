@@ -1,8 +1,10 @@
 // Compiled decode kernels over a window and the sequence's first tokens (PASS 1):
 // int8 K/V, head dims 64 and 128, group sizes 1..16. Warps, ring stages and blocks
-// per item are the plain decode's. Bound by instruction issue (as that one): 4 sequences of
-// 32768..131072 tokens, 32 / 8 heads of 128, a window of 65536 and 500 first tokens: 90 us on a
-// GB300, 5370 GB/s, 0.79 of the measured copy rate.
+// per item are the plain decode's (three CTAs per SM are asked for up to g = 8 on heads
+// of 64, where the weights' second part would take the registers of the third). Bound by
+// instruction issue (as that one): 4 sequences of 32768..131072 tokens, 32 / 8 heads of
+// 128, a window of 65536 and 500 first tokens: 89.4 us on a GB300, 5370 GB/s, 0.79 of the
+// measured copy rate; 110 with values that all take weights in two parts.
 #include "pa_decode_kernel.cuh"
 
 namespace pa {
@@ -16,7 +18,7 @@ struct PolOf<128, G> {
 };
 template <int G>
 struct PolOf<64, G> {
-    using type = QuantMmaPolicy<8, 64, G, 4, 4, (G > 4 ? 1 : 3), 2, 1, false>;
+    using type = QuantMmaPolicy<8, 64, G, 4, 4, (G > 8 ? 1 : 3), 2, 1, false>;
 };
 
 template <int D, int G>
