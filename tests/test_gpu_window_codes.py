@@ -1,6 +1,9 @@
 """pa_window_decode over INT8 and INT4 pools at the tolerance of every operator here,
 |d| <= 1e-2 (1 + |ref|) per element, over the dynamic ranges that real K/V reach
-(workloads.PROFILES)."""
+(workloads.PROFILES), and at the tolerance of its own arithmetic (tests/plain_window_codes.py),
+which a block left out does not pass."""
+import math
+
 import pytest
 import torch
 
@@ -8,8 +11,10 @@ import paged_kv_cache_94_gb300 as pa
 from tests.gpu_helpers import assert_close, gpu_pool
 from tests.plain_attention import gather_rows
 from tests.plain_window import attend_seen, seen_keys
+from tests.plain_window_codes import check_codes
 from tests.range_cases import HEAD_DIMS, PROFILES, workload
-from tests.test_gpu_window_decode import case, decode
+from tests.test_gpu_evict import poison
+from tests.test_gpu_window_decode import case, decode, give_back
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -38,6 +43,41 @@ def test_dynamic_range(kv, d_h, profile):
                 assert st == 0
                 what = f"g{g} window{window}+{n_first} ctas{num_ctas}"
                 assert_close(out.float().cpu().numpy(), ref.numpy(), what)
+                check_codes(out, q, pool, table, ctx, w.scale, window, n_first)
+
+
+@pytest.mark.parametrize("window,n_first", [(0, 0), (1, 4), (130, 0), (200, 150), (64, 5000), (48, 33)])
+@pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", ["int8", "int4"])
+def test_ragged_contexts(kv, d, g, window, n_first):
+    """Values of an ordinary size, and V scales 40 and 1000 times that here and there: items of
+    one part, of two, and runs that change from one to the other."""
+    ctx = [1, 0, 17, 33, 64, 65, 130, 500, 3001, 16, 48, 49]
+    q, _, pool, bt = case(kv, d, g, 2, [1] * len(ctx), ctx, seed=50 + g)
+    poison(pool, bt, ctx)
+    bt = give_back(bt, ctx, [1] * len(ctx), window, n_first)
+    scale = 1 / math.sqrt(d)
+    gen = torch.Generator().manual_seed(51)
+    plain = pool[3].clone()
+    for factors in ((1.0,), (1.0, 1.0, 40.0), (1.0, 0.01, 1000.0)):
+        pick = torch.randint(0, len(factors), plain.shape[:2], generator=gen)
+        pool[3] = plain * torch.tensor(factors)[pick].to(DEV)[..., None]
+        for num_ctas in (0, 1, 7):
+            out, st = decode(q, pool, bt, ctx, scale, window, n_first, num_ctas=num_ctas)
+            assert st == 0
+            check_codes(out, q, pool, bt, ctx, scale, window, n_first)
+
+
+@pytest.mark.parametrize("kv", ["int8", "int4"])
+def test_long_contexts(kv):
+    ctx = [40000, 9001, 20016]
+    q, _, pool, bt = case(kv, 128, 4, 2, [1] * 3, ctx, seed=52)
+    for window, n_first in ((0, 0), (16000, 500)):
+        for num_ctas in (0, 3):
+            out, st = decode(q, pool, bt, ctx, 0.09, window, n_first, num_ctas=num_ctas)
+            assert st == 0
+            check_codes(out, q, pool, bt, ctx, 0.09, window, n_first)
 
 
 @pytest.mark.parametrize("kv", ["int8", "int4"])
