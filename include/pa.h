@@ -541,7 +541,10 @@ pa_status pa_rope_write(const void *q, int64_t q_stride, const void *k, int64_t 
  * between the block of position n_first - 1 and the first one of the first new token's
  * window may have been given back (pa_allocator_free on them, and the sequence goes on
  * appending). K and V that a token does not see do not reach its row,
- * whatever they hold; entries that are not finite make infinity or NaN of what sees them.
+ * whatever they hold. Of what it sees, a V entry that is not finite makes infinity or NaN of its
+ * column; K acts through the scores as in softmax: minus infinity has weight 0; plus infinity,
+ * NaN, or minus infinity alone make the row NaN. (A bad block's tokens are not there: a row
+ * of zeros where it sees no other.)
  * Every other argument is pa_cross_attention's, the workspace's size
  * pa_window_attention_workspace_size(geom, num_ctas); out meets no memory of q
  * (PA_ERR_SHAPE). Accumulation and the weights'
@@ -570,7 +573,8 @@ size_t pa_window_attention_workspace_size(pa_geom geom, int32_t num_ctas);
  * Over INT8 and INT4 pools a weight times its V scale enters the products as one fp16 value
  * (2^-11 relative, or 2^-25 of the largest scale's), in two parts (2^-21) with 32 tokens of
  * which a value may pass 8 in magnitude: results stay within 1e-2 (1 + |ref|) where V rows of
- * many magnitudes cancel. pa_decode has one part, whatever the values.
+ * many magnitudes cancel. pa_decode has one part, whatever the values. K that is not finite acts
+ * as in pa_window_attention, where pa_decode makes zeros of such rows.
  *
  *   window, n_first  >= 0 (PA_ERR_SHAPE)
  *   num_ctas         0: one wave of resident CTAs; > 0: that many

@@ -576,6 +576,11 @@ __device__ __forceinline__ uint32_t seen_keys(const CrossParams &q, int p, int k
            (bits_below(q.n_first - k) | ~bits_below(window_from(q, p) - k));
 }
 
+// WIN: the base of a row whose keys so far all scored minus infinity. Its weights sum to 0, like
+// those of a row that has seen no key (base minus infinity), but it comes out as NaN, as
+// softmax makes of it, and not as zeros. Any other score moves the base.
+constexpr float kNoWeight = -3.402823466e38f;
+
 // One step of the online softmax over 64 keys of an INT8/INT4 tile, of a warp's 32 rows. A
 // thread has four rows, lane / 4 + 8 i, and two of every eight keys: each scale that it loads
 // serves four rows: 16 loads of 8 bytes a step where a row per thread takes 32 of 16 (the INT8
@@ -611,21 +616,26 @@ __device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float 
         }
     }
     bool odd = false; // WIN: a masked step with V scales that are not finite
+    bool some[4] = {true, true, true, true}; // WIN: the row sees a key of the step
     if (WIN && bad >= 0) {
-        uint32_t gone = 0; // a bit for each eight keys
+        uint32_t gone[2]; // the keys of bad blocks
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-            gone |= (bad >> b) & 1 ? 3u << (2 * b) : 0u;
+        for (int w = 0; w < 2; ++w)
+            gone[w] = ((bad >> (2 * w)) & 1 ? 0x0000ffffu : 0u) |
+                      ((bad >> (2 * w + 1)) & 1 ? 0xffff0000u : 0u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at_row = p0 + ((row + 8 * i) >> p.log2_g);
-            const uint32_t seen[2] = {seen_keys(p, at_row, k0) >> c2,
-                                      seen_keys(p, at_row, k0 + 32) >> c2};
+            uint32_t seen[2] = {seen_keys(p, at_row, k0) & ~gone[0],
+                                seen_keys(p, at_row, k0 + 32) & ~gone[1]};
+            some[i] = (seen[0] | seen[1]) != 0;
+            seen[0] >>= c2;
+            seen[1] >>= c2;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (!((seen[k / 4] >> (8 * (k % 4) + e)) & 1) || ((gone >> k) & 1))
+                    if (!((seen[k / 4] >> (8 * (k % 4) + e)) & 1))
                         s[at(i, k) + e] = -INFINITY;
         }
         float sum = 0.f;
@@ -659,7 +669,7 @@ __device__ __forceinline__ void quad_step(uint32_t tS, uint32_t tO, const float 
         top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
         // (WIN: while a row has seen no key its O is zero, on whatever base)
         if (WIN ? m[i] == -INFINITY : first)
-            m[i] = top[i];
+            m[i] = WIN && some[i] ? fmaxf(top[i], kNoWeight) : top[i];
         up = up || top[i] > m[i] + kMoveLog2;
     }
     if (__any_sync(0xffffffffu, up)) {
@@ -1021,6 +1031,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         float mul = !WIN                  ? p.scale_log2
                                     : p.scale_log2 == 0.f ? 1.1754944e-38f
                                                           : fabsf(p.scale_log2);
+                        bool some = true; // WIN: the row sees a key of the step
                         if (WIN && (masked || bad)) {
                             uint32_t seen[2];
 #pragma unroll
@@ -1031,6 +1042,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                 gone |= here & 2 ? 0xffff0000u : 0u;
                                 seen[w] = seen_keys(p, pos, j * kRows + c0 + 32 * w) & ~gone;
                             }
+                            some = (seen[0] | seen[1]) != 0;
 #pragma unroll
                             for (int c = 0; c < kPart; ++c)
                                 s[c] = (seen[c / 32] >> (c % 32)) & 1 ? s[c] : -INFINITY;
@@ -1055,7 +1067,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                                             fmaxf(mx[2], mx[3])));
                         // (WIN: while a row has seen no key its O is zero, on whatever base)
                         if (WIN && m == -INFINITY)
-                            m = top;
+                            m = some ? fmaxf(top, kNoWeight) : top;
                         if (!WIN && first) {
                             m = top;
                         } else {
@@ -1146,6 +1158,10 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 if (lane == 0)
                     poison_rows[warp] = rows;
             }
+            // The reciprocal of what a row's weights sum to (WIN: see kNoWeight)
+            auto inverse = [](float m, float l) {
+                return (WIN ? m != -INFINITY : l > 0.f || l != l) ? 1.f / l : 0.f;
+            };
             // 32 outputs from column c on, of a row whose weights sum to l
             auto emit = [&](int c, float (&o)[32], float inv) {
                 if (L::kCheck && __builtin_expect(poisoned, 0)) {
@@ -1193,7 +1209,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             if (two) {
                 wait(o_full + 8 * half, n_s - 1);
                 tc_fence_after();
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const float inv = inverse(m, l);
 #pragma unroll 1
                 for (int c = 0; !dead && c < D; c += 32) {
                     float o[32];
@@ -1219,7 +1235,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const float f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
                 const float f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - m);
                 l = fmaf(f0, s0.y, f1 * s1.y);
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const float inv = inverse(m, l);
 #pragma unroll 1
                 for (int c = half * (D / 2); !dead && c < (half + 1) * (D / 2); c += 32) {
                     float o[32];
@@ -1288,7 +1304,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float L = st[e].l, inv = L > 0.f || L != L ? 1.f / L : 0.f;
+                    const float inv = inverse(st[e].m, st[e].l);
                     const float *o = st[e].o;
                     const int64_t pr = g.row0 + rr[e];
                     *reinterpret_cast<uint4 *>(

@@ -147,6 +147,21 @@ __device__ __forceinline__ int32_t skipped_blocks(const DecodeParams &p, int32_t
     return max(0, seq_first_block(p, ctx) - kept_blocks(p));
 }
 
+// Pass 1: whether a block of [0, kept) or [lo, last], up to `last`, is in the pool, for a
+// row whose weights sum to 0: then its scores were all minus infinity, which softmax makes
+// NaN of, else there were none. Out of line: it runs next to never.
+static __device__ __noinline__ bool sees_a_block(const int32_t *table, int64_t num_blocks,
+                                                 int32_t kept, int32_t lo, int32_t last)
+{
+#pragma unroll 1
+    for (int32_t i = last; i >= 0; i = i == lo && kept < lo ? kept - 1 : i - 1) {
+        const int32_t phys = __ldg(table + i);
+        if (phys >= 0 && phys < num_blocks)
+            return true;
+    }
+    return false;
+}
+
 __device__ __forceinline__ void flag_error(int32_t *dev_status, int32_t bit)
 {
     if (dev_status)
@@ -541,14 +556,29 @@ __device__ __forceinline__ int64_t unit_row(const DecodeParams &p, int s, int kv
     }
 }
 
-// Final output of d and d + 1 (d even) of query row h: one bf16x2 store.
+// Final output of d and d + 1 (d even) of query row h: one bf16x2 store. none: what
+// a row gets whose weights do not sum to more than 0.
 template <int D, int GQ, int NQ>
 __device__ __forceinline__ void emit2(const DecodeParams &p, int b, int kvh, int h, int d, float L,
-                                      float O0, float O1)
+                                      float O0, float O1, float none = 0.f)
 {
     const size_t row = qo_row<GQ, NQ>(p, b, kvh, h);
     *reinterpret_cast<__nv_bfloat162 *>(p.out + row * D + d) =
-        __floats2bfloat162_rn(L > 0.f ? O0 / L : 0.f, L > 0.f ? O1 / L : 0.f);
+        __floats2bfloat162_rn(L > 0.f ? O0 / L : none, L > 0.f ? O1 / L : none);
+}
+
+// Pass 1: emit2's none. A sum that is not a number stays that; one of 0 is NaN where the
+// token sees a block.
+__device__ __forceinline__ float without_weight(const DecodeParams &p, int b, float L)
+{
+    if (L > 0.f)
+        return 0.f;
+    const int32_t ctx = __ldg(p.context_lens + b);
+    if (L == 0.f && !sees_a_block(p.block_tables + (size_t)b * p.max_blocks, p.num_blocks,
+                                  kept_blocks(p), seq_first_block(p, ctx),
+                                  (ctx - 1) / kBlockTokens))
+        return 0.f;
+    return __int_as_float(0x7fffffff);
 }
 
 // Log-sum-exp state of a run of RUN adjacent d of one row, merged from
@@ -632,7 +662,9 @@ __device__ __forceinline__ void emit_ml(const DecodeParams &p, int b, int kvh, i
     p.ml[qo_row<GQ, NQ>(p, b, kvh, h)] = make_float2(M, L != 0.f ? 1.f / L : 0.f);
 }
 
-template <int D, int GQ, int NW, int NQ, bool MASS = false>
+// WIN (pass 1): rows whose scores are not finite are what softmax gives; elsewhere
+// they are zeros.
+template <int D, int GQ, int NW, int NQ, bool MASS = false, bool WIN = false>
 __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int32_t *P,
                                                const float *merge, int32_t *misc, float *sink_sc,
                                                int b, int kvh, int nb, int64_t Wv, int64_t G,
@@ -662,6 +694,10 @@ __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int3
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             mw[w] = merge[(w * GQ + h) * REC];
+            if constexpr (WIN) { // (a sum that is not a number must not be skipped for its base)
+                const float l = merge[(w * GQ + h) * REC + 1];
+                mw[w] = l != l ? fmaxf(mw[w], 0.f) : mw[w];
+            }
             M = fmaxf(M, mw[w]);
         }
         for (int j = 0; j < ns; ++j)
@@ -695,9 +731,12 @@ __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int3
             if constexpr (MASS)
                 if (d0 == 0)
                     emit_ml<GQ, NQ>(p, b, kvh, h, M, L);
+            float none = 0.f;
+            if constexpr (WIN)
+                none = without_weight(p, b, L);
 #pragma unroll
             for (int e = 0; e < RUN; e += 2)
-                emit2<D, GQ, NQ>(p, b, kvh, h, d0 + e, L, O[e], O[e + 1]);
+                emit2<D, GQ, NQ>(p, b, kvh, h, d0 + e, L, O[e], O[e + 1], none);
         } else {
             if (d0 == 0) {
                 rec[h * REC] = M;
@@ -733,9 +772,12 @@ __device__ __forceinline__ void finish_segment(const DecodeParams &p, const int3
     if constexpr (MASS)
         if (d0 == 0)
             emit_ml<GQ, NQ>(p, b, kvh, h, st.M, st.L);
+    float none = 0.f;
+    if constexpr (WIN)
+        none = without_weight(p, b, st.L);
 #pragma unroll
     for (int e = 0; e < RUN; e += 2)
-        emit2<D, GQ, NQ>(p, b, kvh, h, d0 + e, st.L, st.O[e], st.O[e + 1]);
+        emit2<D, GQ, NQ>(p, b, kvh, h, d0 + e, st.L, st.O[e], st.O[e + 1], none);
 }
 
 // ---------------------------------------------------------------------------

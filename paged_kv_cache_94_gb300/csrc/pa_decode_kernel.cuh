@@ -620,9 +620,9 @@ __global__ void __launch_bounds__(Pol::NW * 32, Pol::kMinBlocks)
         if constexpr (PASS == 2)
             finish_fused<D, GQ, NW>(p, P, merge, misc, b_cur, kvh_cur, Wv, G, whole);
         else
-            finish_segment<D, GQ, NW, Pol::NQ, MASS>(p, P, merge, misc, sink_sc, b_cur, kvh_cur,
-                                               (int)nb_cur, Wv, G, whole, ws,
-                                               s_hi > ws ? s_hi : ws);
+            finish_segment<D, GQ, NW, Pol::NQ, MASS, PASS == 1>(
+                p, P, merge, misc, sink_sc, b_cur, kvh_cur, (int)nb_cur, Wv, G, whole, ws,
+                s_hi > ws ? s_hi : ws);
         seg_lo = seg_hi;
     }
 
