@@ -180,8 +180,10 @@ pa_status pa_decode_workspace_init(void *workspace, size_t workspace_bytes, void
  * counts the whole history INCLUDING the new token, which the caller appends
  * with pa_cache_write first. INT8 rows are read as code * scale (fp32),
  * [G] §4.2 `dequantize_kv`. The pages use scale = 1 / sqrt(d_h).
- * Accumulation is fp32; the output is rounded to bf16. ctx_b == 0 gives a
- * zero row. Long contexts are split across CTAs and merged with a
+ * Accumulation is fp32; the output is rounded to bf16. Over INT8 and INT4 pools a
+ * weight times its V scale is one fp16 value: 2^-11 of the weighted mean of |V|,
+ * which shows where few tokens' V of many magnitudes cancel (pa_window_decode
+ * has two). ctx_b == 0 gives a zero row. Long contexts are split across CTAs and merged with a
  * log-sum-exp reduction, so results do not depend on how the work was split
  * beyond fp32 rounding.
  *

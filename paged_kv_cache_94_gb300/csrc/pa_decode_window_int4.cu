@@ -1,8 +1,10 @@
 // Compiled decode kernels over a window and the sequence's first tokens (PASS 1):
 // int4 K/V, head dims 64 and 128, group sizes 1..16. Warps, ring stages and blocks
-// per item are the plain decode's. Bound by instruction issue (as that one): 96 sequences of
-// 1..3001 tokens, 16 heads of 64, g = 1, a window of 1001 and 20 first tokens: 54 us on a GB300,
-// 1730 GB/s, 0.26 of the measured copy rate (one of the contraction's eight columns is live).
+// per item are the plain decode's. 96 sequences of 1..3001 tokens, 16 heads of 64,
+// g = 1, a window of 1001 and 20 first tokens: 54 us on a GB300, 1730 GB/s, 0.26 of the measured
+// copy rate; bound by its instructions (one of the contraction's eight columns is live) and their
+// latency: with 11 warps per SM the issue slots are 50% busy, most of the rest fixed latencies
+// between dependent instructions. 61 with values that all take weights in two parts.
 #include "pa_decode_kernel.cuh"
 
 namespace pa {

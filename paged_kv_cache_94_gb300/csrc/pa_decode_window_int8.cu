@@ -1,10 +1,11 @@
 // Compiled decode kernels over a window and the sequence's first tokens (PASS 1):
 // int8 K/V, head dims 64 and 128, group sizes 1..16. Warps, ring stages and blocks
 // per item are the plain decode's (three CTAs per SM are asked for up to g = 8 on heads
-// of 64, where the weights' second part would take the registers of the third). Bound by
-// instruction issue (as that one): 4 sequences of 32768..131072 tokens, 32 / 8 heads of
-// 128, a window of 65536 and 500 first tokens: 89.4 us on a GB300, 5370 GB/s, 0.79 of the
-// measured copy rate; 110 with values that all take weights in two parts.
+// of 64, where the weights' second part would take the registers of the third). 4 sequences
+// of 32768..131072 tokens, 32 / 8 heads of 128, a window of 65536 and 500 first tokens: 90
+// us on a GB300, 5400 GB/s, 0.79 of the measured copy rate; bound by its instructions and
+// their latency (8 warps per SM, issue slots 50% busy). 110 with values that all take
+// weights in two parts.
 #include "pa_decode_kernel.cuh"
 
 namespace pa {

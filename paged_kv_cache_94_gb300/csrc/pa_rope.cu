@@ -18,8 +18,9 @@
 // Measured on a GB300, launches back to back: 8192 tokens of 32 + 8 heads of 128 into a bf16
 // pool 37.7 us, 5340 GB/s, 0.79 of the measured copy rate (56 with rows found by division and
 // 98 registers, two CTAs per SM; 39 with angles in double precision); into an INT8 pool 42.
-// 4111 tokens of 16 + 16 heads of 64 into an INT8 pool 13.1 us (21.5 where one near half had
-// all eight values divided, 18.7 with a division each). A step of 64 tokens 2.8 us.
+// 4111 tokens of 16 + 16 heads of 64 into an INT8 pool 12.8 us, INT4 12.5, bf16 8.6 (INT8 21.5
+// where one near half had all eight values divided, 18.7 with a division each); issue slots 62%
+// busy, most of a warp's time ready and not picked. A step of 64 tokens 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
